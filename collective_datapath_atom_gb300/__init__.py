@@ -17,10 +17,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpurlin.so")
 
 PURLIN_MAX_RANKS = 64
+PURLIN_MAX_GROUPS = 1024
 
-PURLIN_F32, PURLIN_BF16 = 0, 1
+PURLIN_F32, PURLIN_BF16, PURLIN_E4M3 = 0, 1, 2
 PURLIN_COPY, PURLIN_SUM = 0, 1
 PURLIN_PACKED, PURLIN_SCATTERED, PURLIN_TRANSPOSED = 0, 1, 2
+PURLIN_WEIGHTS_NK, PURLIN_WEIGHTS_KN = 0, 1
 
 PURLIN_OK = 0
 PURLIN_ERR_INVALID_ARG = 1
@@ -116,6 +118,7 @@ class PurlinError(RuntimeError):
 # Exported symbols and their C signatures (kept in step with include/purlin.h).
 _VPP = ctypes.POINTER(ctypes.c_void_p)
 _SZP = ctypes.POINTER(ctypes.c_size_t)
+_VP, _SZ = ctypes.c_void_p, ctypes.c_size_t
 _CTX = ctypes.c_void_p
 _SIGNATURES = {
     "purlin_init": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(_CTX)]),
@@ -148,6 +151,18 @@ _SIGNATURES = {
                                                  ctypes.c_int, ctypes.c_int, purlin_layout,
                                                  ctypes.c_void_p]),
     "purlin_noalloc_check": (ctypes.c_int, [ctypes.c_void_p]),
+    "purlin_rms_norm": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, ctypes.c_float,
+        ctypes.c_int, ctypes.c_int]),
+    "purlin_rms_norm_backward": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, ctypes.c_float,
+        ctypes.c_int]),
+    "purlin_grouped_matmul": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _VP, _VP, _VP, ctypes.c_int, _SZ, _SZ, _SZ,
+        ctypes.c_int, ctypes.c_int]),
+    "purlin_grouped_matmul_weight_grad": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _VP, ctypes.c_int, _SZ, _SZ, _SZ,
+        ctypes.c_int]),
     "purlin_empty_launch": (ctypes.c_int, [ctypes.c_void_p]),
     "purlin_touch_launch": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "purlin_check": (ctypes.c_int, [_CTX]),
@@ -369,6 +384,51 @@ def purlin_noalloc_check(stream=None):
     """Synchronize `stream` and raise if a device-side wait of an
     allocation-free AllReduce expired since the last check."""
     _ok(lib.purlin_noalloc_check(ctypes.c_void_p(_stream_handle(stream))), "purlin_noalloc_check")
+
+
+# ------------------------------------------------------ layer operators ---
+
+def purlin_rms_norm(ctx, x, weight, y, rows, hidden, eps, dtype, out_dtype=None, residual=None,
+                    total=None, scales=None, ldx=0, ldr=0, ldy=0, ldt=0):
+    """Norm of ``x + residual``; ``out_dtype`` (default ``dtype``) PURLIN_E4M3
+    writes 8-bit rows and ``scales``.  Strides 0: contiguous rows."""
+    st = lib.purlin_rms_norm(ctx.handle, _addr(x), ldx, _addr(residual), ldr, _addr(weight),
+                             _addr(y), ldy, _addr(total), ldt, _addr(scales), rows, hidden, eps,
+                             dtype, dtype if out_dtype is None else out_dtype)
+    if st:
+        _ok(st, "purlin_rms_norm")
+
+
+def purlin_rms_norm_backward(ctx, dy, total, weight, dx, dweight, rows, hidden, eps, dtype,
+                             dtotal=None, lddy=0, ldt=0, lddt=0, lddx=0):
+    """Gradients of :func:`purlin_rms_norm` at ``total``; ``dweight`` is float32."""
+    st = lib.purlin_rms_norm_backward(ctx.handle, _addr(dy), lddy, _addr(total), ldt,
+                                      _addr(weight), _addr(dtotal), lddt, _addr(dx), lddx,
+                                      _addr(dweight), rows, hidden, eps, dtype)
+    if st:
+        _ok(st, "purlin_rms_norm_backward")
+
+
+def purlin_grouped_matmul(ctx, x, w, y, begin, count, groups, rows, n, k, dtype,
+                          layout=PURLIN_WEIGHTS_NK, x_scales=None, w_scales=None, ldx=0, ldw=0,
+                          ldy=0):
+    """Products grouped by expert; ``begin`` and ``count`` are device int64
+    arrays (tensors or addresses) of each group's first row and row count."""
+    st = lib.purlin_grouped_matmul(ctx.handle, _addr(x), ldx, _addr(w), ldw, _addr(y), ldy,
+                                   _addr(x_scales), _addr(w_scales), _addr(begin), _addr(count),
+                                   groups, rows, n, k, dtype, layout)
+    if st:
+        _ok(st, "purlin_grouped_matmul")
+
+
+def purlin_grouped_matmul_weight_grad(ctx, dy, x, dw, begin, count, groups, rows, n, k, dtype,
+                                      lddy=0, ldx=0, lddw=0):
+    """Weight gradient of :func:`purlin_grouped_matmul`: ``dw`` is groups x n x k."""
+    st = lib.purlin_grouped_matmul_weight_grad(ctx.handle, _addr(dy), lddy, _addr(x), ldx,
+                                               _addr(dw), lddw, _addr(begin), _addr(count),
+                                               groups, rows, n, k, dtype)
+    if st:
+        _ok(st, "purlin_grouped_matmul_weight_grad")
 
 
 def purlin_empty_launch(stream=None):

@@ -514,6 +514,7 @@ purlin_status purlin_finalize(purlin_ctx *ctx) {
         if (m.staging) cudaFree(m.staging);
         if (m.state) cudaFree(m.state);
     }
+    free_workspace(ctx);
     if (ctx->flags) cudaFree(ctx->flags);
     if (ctx->packets) cudaFree(ctx->packets);
     if (ctx->err) cudaFree(ctx->err);

@@ -91,6 +91,15 @@ struct CacheEntry {
     bool pinned = false;   // used while a CUDA graph was captured: kept until finalize
 };
 
+// Device memory that one call at a time uses for partial results; `next`
+// chains buffers that outgrown ones leave behind for captured graphs.
+struct WorkMem {
+    void *p = nullptr;
+    size_t bytes = 0;
+    bool pinned = false;   // used while a CUDA graph was captured: kept until finalize
+    WorkMem *next = nullptr;
+};
+
 // True while a CUDA graph is being captured from stream s.
 bool capturing(cudaStream_t s);
 
@@ -128,6 +137,8 @@ struct purlin_ctx {
     std::unordered_map<std::string, std::list<purlin::host::CacheEntry>::iterator> index;
     std::list<purlin::host::DeviceCollMem> device_colls;   // memory of purlin_device_prepare descriptors
     std::list<purlin::host::ChannelMem> channels;          // memory of packet channels
+    purlin::host::WorkMem work;                 // the layer operators' partial results
+    purlin::host::WorkMem *old_work = nullptr;  // outgrown, kept for captured graphs
 };
 
 namespace purlin {
@@ -139,6 +150,8 @@ void flag_geometry(uint64_t notify_chunks, uint64_t nchunks, int64_t grid, uint3
                    uint64_t *epoch_inc);
 int ring_ar_mode(const purlin_ctx *ctx);
 Policy call_policy(const purlin_ctx *ctx, const CallDesc &c);
+purlin_status workspace(purlin_ctx *ctx, size_t bytes, void **out);   // layers_api.cpp
+void free_workspace(purlin_ctx *ctx);
 
 }  // namespace host
 }  // namespace purlin

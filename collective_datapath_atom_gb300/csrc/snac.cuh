@@ -65,6 +65,8 @@ enum ErrSite : uint64_t {
     kSiteDeviceCounts = 6, // device-resident counts that exceed the declared capacities
     kSitePacketWait = 7,   // a latency-path packet that never arrived
     kSiteChannelArgs = 8,  // a packet-channel unit past the channel's capacity
+    kSiteGroups = 9,       // a group of a grouped product that lies outside its rows
+    kSiteGroupedWait = 10, // a tile of a grouped product that never arrived
 };
 
 struct Ctl {

@@ -70,7 +70,10 @@ extern "C" {
 typedef struct purlin_ctx purlin_ctx;   /* opaque; created by purlin_init */
 typedef void *purlin_stream;            /* a cudaStream_t (NULL = legacy default stream) */
 
-typedef enum { PURLIN_F32 = 0, PURLIN_BF16 = 1 } purlin_dtype;
+/* The collectives take F32 and BF16.  E4M3 (8 bits: 4 exponent, 3 mantissa
+ * bits, largest value 448, no infinities) is a type of the layer operators
+ * only; its bytes travel through a collective as pairs, like bf16. */
+typedef enum { PURLIN_F32 = 0, PURLIN_BF16 = 1, PURLIN_E4M3 = 2 } purlin_dtype;
 
 /* The consume operation of a collective (§3.1): copy or reduce (sum). */
 typedef enum { PURLIN_COPY = 0, PURLIN_SUM = 1 } purlin_op;
@@ -257,6 +260,109 @@ purlin_status purlin_all_reduce_noalloc(int R, const void *const src[], void *co
  * synchronize or the 8-byte copy fails (a device fault).  Not during stream
  * capture.  Allocates nothing. */
 purlin_status purlin_noalloc_check(purlin_stream stream);
+
+/* -------------------------------------------------------- layer operators */
+
+/* What a language model's layer computes directly after the collectives: the
+ * norm that consumes an AllReduce (the residual's addition in it), and the
+ * experts' products that consume an AllToAllV dispatch, each with its
+ * backward pass.  They are calls on one rank's buffers; loop over the ranks
+ * as the buffers are laid out.
+ *
+ * Shared conventions.  Matrices are row-major; `ld*` is the distance between
+ * rows in elements, and 0 means contiguous rows.  All pointers are DEVICE
+ * pointers.  Calls enqueue on the context's stream and return; argument
+ * errors are reported before anything is enqueued.  Sums and statistics are
+ * binary32; each output is rounded once.  Results do not depend on timing:
+ * the same inputs give the same bits.  Partial results go to a workspace the
+ * context owns, grown by the first call that needs more: during graph capture
+ * such a call returns UNSUPPORTED, so make it once before.  rows, hidden, n
+ * and k are below 2^31; offsets within a matrix may exceed 32 bits.  An
+ * output may not overlap another buffer (ALIAS) except where stated. */
+
+/* Root-mean-square norm with the residual's addition, for each row:
+ *   t = x + residual   (residual NULL: t = x)
+ *   v = t / sqrt(mean(t^2) + eps) * weight
+ * out_dtype == dtype: y = v, and scales must be NULL.  out_dtype E4M3:
+ * scales[row] = max(max |v| / 448, 2^-126) and y = v / scales[row] in e4m3
+ * (nearest even; the maximum skips NaN, and a NaN element is e4m3 NaN).  An
+ * all-zero row gives zeros.  total (or NULL) receives t: the residual stream
+ * of the next layer.  The norm is of the unrounded t.
+ * dtype F32 or BF16, that of x, residual, weight and total.  Pointers need
+ * only their type's alignment; rows on 16-byte boundaries take 128-bit
+ * accesses.  total may be x or residual, and y may be x or residual when the
+ * types are equal (same pointer and ld).  rows == 0 is a no-op.
+ * Errors: INVALID_ARG (NULL, hidden 0, ld < hidden, eps negative or not
+ * finite, scales given or missing), UNSUPPORTED (other out_dtype),
+ * ALIGNMENT, ALIAS, CUDA. */
+purlin_status purlin_rms_norm(purlin_ctx *ctx, const void *x, size_t ldx, const void *residual,
+                              size_t ldr, const void *weight, void *y, size_t ldy, void *total,
+                              size_t ldt, float *scales, size_t rows, size_t hidden, float eps,
+                              purlin_dtype dtype, purlin_dtype out_dtype);
+
+/* Gradient of purlin_rms_norm at t = total (as the forward pass left it).
+ * dy: gradient of y; dtotal: gradient of total from the layers above, or
+ * NULL.  With g = dy * weight and r = 1 / sqrt(mean(t^2) + eps):
+ *   dx = r * (g - t * r^2 * mean(g * t)) + dtotal    (of x and of residual)
+ *   dweight[j] = sum over rows of dy * t * r         (F32, overwritten)
+ * dx may be dy, total or dtotal (same pointer and ld).  rows == 0 sets
+ * dweight to zero.  Errors as for purlin_rms_norm, plus OOM (workspace) and
+ * UNSUPPORTED during capture (above). */
+purlin_status purlin_rms_norm_backward(purlin_ctx *ctx, const void *dy, size_t lddy,
+                                       const void *total, size_t ldt, const void *weight,
+                                       const void *dtotal, size_t lddt, void *dx, size_t lddx,
+                                       float *dweight, size_t rows, size_t hidden, float eps,
+                                       purlin_dtype dtype);
+
+/* How the weights of a grouped product lie in memory. */
+typedef enum {
+    PURLIN_WEIGHTS_NK = 0,   /* groups matrices of n x k: y = x w^T */
+    PURLIN_WEIGHTS_KN = 1    /* groups matrices of k x n: y = x w */
+} purlin_weights_layout;
+
+#define PURLIN_MAX_GROUPS 1024
+
+/* Matrix products grouped by expert.  Group g is the `count[g]` rows of x
+ * from row begin[g] on, and
+ *   y[i][j] = sum over c of x[i][c] * w_g[j][c]      (PURLIN_WEIGHTS_NK)
+ *   y[i][j] = sum over c of x[i][c] * w_g[c][j]      (PURLIN_WEIGHTS_KN)
+ * for its rows i; the sum is binary32 (the order is the tensor cores'),
+ * rounded once to y, which is BF16.  The matrices w_g lie one after another,
+ * rows ldw apart.  KN on the same weights, with dy in place of x, is the
+ * gradient with respect to x.
+ * begin and count are DEVICE arrays of `groups` entries, read in stream
+ * order, 8-byte aligned: an AllToAllV with device counts needs no host round
+ * trip, and its capacity-padded outputs no compaction.  Groups may be empty
+ * and in any order, but may not overlap; rows of y in no group are not
+ * written, and rows of x in none do not matter, whatever they hold.  The
+ * kernel checks begin[g] >= 0, count[g] >= 0, begin[g] + count[g] <= rows
+ * and sum(count) <= rows; otherwise it writes nothing and records
+ * INVALID_ARG in the context's error word (purlin_check).
+ * dtype BF16 (scales NULL) or E4M3 (NK only): then y is multiplied by
+ * x_scales[i] * w_scales[g * n + j] before it is rounded.
+ * x and w are 16-byte aligned and so are their rows (ldx, ldw times the
+ * element size a multiple of 16; k and n themselves may be odd); y needs 2
+ * bytes.  rows, n or groups == 0 is a no-op.
+ * Errors: INVALID_ARG (NULL, groups out of 0..PURLIN_MAX_GROUPS, k 0, ld too
+ * small, scales given or missing), UNSUPPORTED (F32; E4M3 with KN; more than
+ * 2^31 tiles), ALIGNMENT, ALIAS (y and an input), OOM, CUDA. */
+purlin_status purlin_grouped_matmul(purlin_ctx *ctx, const void *x, size_t ldx, const void *w,
+                                    size_t ldw, void *y, size_t ldy, const float *x_scales,
+                                    const float *w_scales, const int64_t begin[],
+                                    const int64_t count[], int groups, size_t rows, size_t n,
+                                    size_t k, purlin_dtype dtype, purlin_weights_layout layout);
+
+/* Weight gradient of purlin_grouped_matmul (NK weights):
+ *   dw_g[j][c] = sum over the rows i of group g of dy[i][j] * x[i][c]
+ * BF16 throughout, the sum in binary32, dw overwritten; an empty group's dw
+ * is zero (all of them when rows == 0).  For KN weights swap dy with x and n
+ * with k.  Groups, checks and alignment (dy, x; dw needs 2 bytes) as above.
+ * n, k or groups == 0 is a no-op. */
+purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy, size_t lddy,
+                                                const void *x, size_t ldx, void *dw, size_t lddw,
+                                                const int64_t begin[], const int64_t count[],
+                                                int groups, size_t rows, size_t n, size_t k,
+                                                purlin_dtype dtype);
 
 /* ------------------------------------------------------------ measurement */
 
