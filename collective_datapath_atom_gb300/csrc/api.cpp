@@ -22,6 +22,7 @@
 
 #include "host.h"
 #include "launch.h"
+#include "layers.h"
 #include "plan.h"
 
 using namespace purlin;
@@ -469,6 +470,7 @@ purlin_status purlin_init(int R, purlin_stream stream, purlin_ctx **out) {
         if (ctx->flags) cudaFree(ctx->flags);
         if (ctx->packets) cudaFree(ctx->packets);
         if (ctx->err) cudaFree(ctx->err);
+        if (ctx->arrived) cudaFree(ctx->arrived);
         delete ctx;
         return s;
     };
@@ -484,14 +486,16 @@ purlin_status purlin_init(int R, purlin_stream stream, purlin_ctx **out) {
     if (cudaMalloc(&ctx->flags, 2 * (size_t)kFlagSlots * sizeof(unsigned long long)) !=
             cudaSuccess ||
         cudaMalloc(&ctx->packets, 2 * kPacketStagingBytes) != cudaSuccess ||
-        cudaMalloc(&ctx->err, 4 * sizeof(unsigned long long)) != cudaSuccess)
+        cudaMalloc(&ctx->err, 4 * sizeof(unsigned long long)) != cudaSuccess ||
+        cudaMalloc(&ctx->arrived, kMaxSms * sizeof(unsigned)) != cudaSuccess)
         return fail(PURLIN_ERR_OOM);
     ctx->dev_epoch = ctx->err + 2;
     if (cudaMemsetAsync(ctx->packets, 0, 2 * kPacketStagingBytes, ctx->stream) != cudaSuccess)
         return fail(PURLIN_ERR_CUDA);
     if (cudaMemsetAsync(ctx->flags, 0, 2 * (size_t)kFlagSlots * sizeof(unsigned long long),
                         ctx->stream) != cudaSuccess ||
-        cudaMemsetAsync(ctx->err, 0, 4 * sizeof(unsigned long long), ctx->stream) != cudaSuccess)
+        cudaMemsetAsync(ctx->err, 0, 4 * sizeof(unsigned long long), ctx->stream) != cudaSuccess ||
+        cudaMemsetAsync(ctx->arrived, 0, kMaxSms * sizeof(unsigned), ctx->stream) != cudaSuccess)
         return fail(PURLIN_ERR_CUDA);
     // the device epoch starts at 1 (flags start at 0, below any epoch)
     static const unsigned long long kFirstEpoch = 1;
@@ -518,6 +522,7 @@ purlin_status purlin_finalize(purlin_ctx *ctx) {
     if (ctx->flags) cudaFree(ctx->flags);
     if (ctx->packets) cudaFree(ctx->packets);
     if (ctx->err) cudaFree(ctx->err);
+    if (ctx->arrived) cudaFree(ctx->arrived);
     delete ctx;
     return st;
 }
@@ -603,7 +608,10 @@ purlin_status purlin_check(purlin_ctx *ctx) {
     if (cudaMemcpy(&word, ctx->err, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
         return PURLIN_ERR_CUDA;
     if (word == 0) return PURLIN_OK;
-    if (cudaMemset(ctx->err, 0, sizeof word) != cudaSuccess) return PURLIN_ERR_CUDA;
+    // a grouped product that gave up may have left its tiles' counters part-way
+    if (cudaMemset(ctx->err, 0, sizeof word) != cudaSuccess ||
+        cudaMemset(ctx->arrived, 0, kMaxSms * sizeof(unsigned)) != cudaSuccess)
+        return PURLIN_ERR_CUDA;
     return static_cast<purlin_status>(word & 0xFF);
 }
 

@@ -71,11 +71,18 @@ struct GroupedArgs {
     size_t rows = 0, n = 0, k = 0;
     int dtype = 0;
     int sms = 0;
+    float *partial = nullptr;       // grouped_workspace(sms) bytes
+    unsigned *arrived = nullptr;    // kMaxSms counters, zero between launches
     unsigned long long *err = nullptr;
     cudaStream_t stream = nullptr;
 };
 
-constexpr int kMaxGroups = 1024;
+constexpr int kMaxGroups = PURLIN_MAX_GROUPS;
+constexpr int kMaxSms = 1024;
+constexpr size_t kGroupedMaxRowTile = 256;   // rows of a tile, channels of a tile
+constexpr size_t kGroupedTileChannels = 128;
+
+size_t grouped_workspace(int sms);
 
 cudaError_t launch_grouped(const GroupedArgs &a);
 

@@ -55,6 +55,30 @@ bool misaligned(const void *p, size_t to) {
 
 bool bad_ld(size_t ld, size_t cols) { return ld < cols || ld > kMaxPitch; }
 
+// Whether a grouped product's tiles (tall: rows, or n for the weight gradient)
+// can be counted in 32 bits, and a weight matrix's pitch in the 40 that a
+// tensor map has.
+bool too_many_tiles(size_t channels, size_t tall, size_t each_group, int groups) {
+    const size_t across = channels / kGroupedTileChannels + 1;
+    const size_t down = tall / kGroupedMaxRowTile + each_group * (size_t)groups;
+    return across * down > kMaxExtent / 2;
+}
+bool too_long(size_t rows, size_t ld, size_t es) {
+    return rows != 0 && ld * es >= ((size_t)1 << 40) / rows;
+}
+
+purlin_status run_grouped(purlin_ctx *ctx, GroupedArgs &a) {
+    void *work = nullptr;
+    const purlin_status st = workspace(ctx, grouped_workspace(ctx->sms), &work);
+    if (st != PURLIN_OK) return st;
+    a.sms = ctx->sms;
+    a.partial = static_cast<float *>(work);
+    a.arrived = ctx->arrived;
+    a.err = ctx->err;
+    a.stream = ctx->stream;
+    return launch_grouped(a) == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA;
+}
+
 }  // namespace
 
 namespace purlin {
@@ -267,6 +291,8 @@ purlin_status purlin_grouped_matmul(purlin_ctx *ctx, const void *x, size_t ldx, 
         overlap(my, matrix(x_scales, 1, rows, rows, PURLIN_F32)) ||
         overlap(my, matrix(w_scales, 1, (size_t)groups * n, (size_t)groups * n, PURLIN_F32)))
         return PURLIN_ERR_ALIAS;
+    if (too_many_tiles(n, rows, 1, groups) || too_long(w_rows, ldw, es))
+        return PURLIN_ERR_UNSUPPORTED;
     if (ctx == nullptr) return PURLIN_ERR_INVALID_ARG;
 
     GroupedArgs a;
@@ -286,10 +312,7 @@ purlin_status purlin_grouped_matmul(purlin_ctx *ctx, const void *x, size_t ldx, 
     a.n = n;
     a.k = k;
     a.dtype = dtype;
-    a.sms = ctx->sms;
-    a.err = ctx->err;
-    a.stream = ctx->stream;
-    return launch_grouped(a) == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA;
+    return run_grouped(ctx, a);
 }
 
 purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy, size_t lddy,
@@ -319,6 +342,7 @@ purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy,
     if (overlap(mw, matrix(dy, rows, n, lddy, dtype)) ||
         overlap(mw, matrix(x, rows, k, ldx, dtype)))
         return PURLIN_ERR_ALIAS;
+    if (too_many_tiles(k, 0, n / kGroupedMaxRowTile + 1, groups)) return PURLIN_ERR_UNSUPPORTED;
     if (ctx == nullptr) return PURLIN_ERR_INVALID_ARG;
     if (rows == 0)
         return cudaMemset2DAsync(dw, lddw * 2, 0, k * 2, (size_t)groups * n, ctx->stream) ==
@@ -341,10 +365,7 @@ purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy,
     a.n = n;
     a.k = k;
     a.dtype = dtype;
-    a.sms = ctx->sms;
-    a.err = ctx->err;
-    a.stream = ctx->stream;
-    return launch_grouped(a) == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA;
+    return run_grouped(ctx, a);
 }
 
 }  // extern "C"
