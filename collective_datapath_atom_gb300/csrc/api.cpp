@@ -487,7 +487,7 @@ purlin_status purlin_init(int R, purlin_stream stream, purlin_ctx **out) {
             cudaSuccess ||
         cudaMalloc(&ctx->packets, 2 * kPacketStagingBytes) != cudaSuccess ||
         cudaMalloc(&ctx->err, 4 * sizeof(unsigned long long)) != cudaSuccess ||
-        cudaMalloc(&ctx->arrived, kMaxSms * sizeof(unsigned)) != cudaSuccess)
+        cudaMalloc(&ctx->arrived, kJoinCounters * sizeof(unsigned)) != cudaSuccess)
         return fail(PURLIN_ERR_OOM);
     ctx->dev_epoch = ctx->err + 2;
     if (cudaMemsetAsync(ctx->packets, 0, 2 * kPacketStagingBytes, ctx->stream) != cudaSuccess)
@@ -495,7 +495,7 @@ purlin_status purlin_init(int R, purlin_stream stream, purlin_ctx **out) {
     if (cudaMemsetAsync(ctx->flags, 0, 2 * (size_t)kFlagSlots * sizeof(unsigned long long),
                         ctx->stream) != cudaSuccess ||
         cudaMemsetAsync(ctx->err, 0, 4 * sizeof(unsigned long long), ctx->stream) != cudaSuccess ||
-        cudaMemsetAsync(ctx->arrived, 0, kMaxSms * sizeof(unsigned), ctx->stream) != cudaSuccess)
+        cudaMemsetAsync(ctx->arrived, 0, kJoinCounters * sizeof(unsigned), ctx->stream) != cudaSuccess)
         return fail(PURLIN_ERR_CUDA);
     // the device epoch starts at 1 (flags start at 0, below any epoch)
     static const unsigned long long kFirstEpoch = 1;
@@ -610,7 +610,7 @@ purlin_status purlin_check(purlin_ctx *ctx) {
     if (word == 0) return PURLIN_OK;
     // a grouped product that gave up may have left its tiles' counters part-way
     if (cudaMemset(ctx->err, 0, sizeof word) != cudaSuccess ||
-        cudaMemset(ctx->arrived, 0, kMaxSms * sizeof(unsigned)) != cudaSuccess)
+        cudaMemset(ctx->arrived, 0, kJoinCounters * sizeof(unsigned)) != cudaSuccess)
         return PURLIN_ERR_CUDA;
     return static_cast<purlin_status>(word & 0xFF);
 }

@@ -4,19 +4,21 @@
 // what A, B, i, j and k are in each mode.  Groups are (first row, row count)
 // pairs in device memory, so the tiles of a launch are found on the device.
 //
-// One persistent CTA an SM.  A tile is 128 i by up to 256 j: the weights'
-// channels take the tensor core's 128-lane side and the group's rows the other,
-// whose width is a field of the instruction, so a group of 5 rows costs a
-// 16-column product, not a padded one, and the same code serves one token and a
-// prefill.  A warp brings 128-byte-wide boxes of both operands into a ring of
-// shared-memory stages (TMA, 128-byte swizzle), a warp issues tcgen05.mma from
-// them into one of two accumulators in tensor memory, and four warps write the
-// other accumulator out meanwhile.
+// Persistent CTAs, one an SM, alone or in pairs that share a tile.  A tile is
+// 128 i (256 for a pair) by up to 256 j: the weights' channels take the tensor
+// core's 128-lane side and the group's rows the other, whose width is a field of
+// the instruction, so a group of 5 rows costs a 16-column product, not a padded
+// one, and the same code serves one token and a prefill.  A warp brings
+// 128-byte-wide boxes of both operands into a ring of shared-memory stages (TMA,
+// 128-byte swizzle), a warp issues tcgen05.mma from them into one of two
+// accumulators in tensor memory, and eight warps write the other accumulator out
+// meanwhile.
 //
-// With fewer tiles than SMs (decode) K is split over the idle CTAs: each
-// writes its binary32 accumulator to a workspace, and the last of a tile's CTAs
-// to arrive adds them in split order, so the result does not depend on which
-// came last.
+// Tiles go round the CTAs in whole waves; what is left over, or everything when
+// there are fewer tiles than CTAs (decode), is cut into equal runs of K blocks
+// instead, one a CTA.  A run's partial tiles go to a workspace in binary32, and
+// the last of a tile's CTAs to arrive adds them in K order, so the result does
+// not depend on which came last.
 //
 // kGroupedGrad sums over a group's rows: both operands then lie along M or N in
 // memory (MN-major), and the last block of rows is cut at the group's end by
@@ -34,144 +36,306 @@
 namespace purlin {
 namespace {
 
-struct GroupTable {
-    int tiles[kMaxGroups + 1];   // tiles before group g
-    int begin[kMaxGroups];
-    int count[kMaxGroups];
-    int most;                    // rows of the largest group
-    int bad;
-};
-
-// Read and check the groups; tiles[g] = tiles before group g, from
-// tiles_of(count).  Every thread of the block calls it; false if a group lies
-// outside the rows or the groups hold more rows than there are (so some
-// overlap).
-template <typename F>
-__device__ bool read_groups(GroupTable &t, const int64_t *begin, const int64_t *count, int groups,
-                            long long rows, F tiles_of) {
-    if (threadIdx.x == 0) t.bad = 0;
-    __syncthreads();
-    for (int g = threadIdx.x; g < groups; g += blockDim.x) {
-        const long long b = begin[g], c = count[g];
-        // c > rows first: b + c does not overflow
-        if (c < 0 || b < 0 || c > rows || b > rows - c) t.bad = 1;
-        t.begin[g] = (int)b;
-        t.count[g] = (int)c;
-    }
-    __syncthreads();
-    if (t.bad) return false;
-    if (threadIdx.x < 32) {
-        int before = 0;
-        long long held = 0;
-        int most = 0;
-        for (int g0 = 0; g0 < groups; g0 += 32) {
-            const int g = g0 + (int)threadIdx.x;
-            int v = g < groups ? tiles_of(t.count[g]) : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if ((int)threadIdx.x >= o) v += u;
-            }
-            if (g < groups) {
-                t.tiles[g + 1] = before + v;
-                held += t.count[g];
-                most = max(most, t.count[g]);
-            }
-            before += __shfl_sync(0xffffffffu, v, 31);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            held += __shfl_xor_sync(0xffffffffu, held, o);
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        }
-        if (threadIdx.x == 0) {
-            t.tiles[0] = 0;
-            t.most = most;
-            if (held > rows) t.bad = 1;
-        }
-    }
-    __syncthreads();
-    return !t.bad;
-}
-
-// The group whose tiles include tile `t` (groups without tiles are skipped).
-__device__ __forceinline__ int group_of(const GroupTable &t, int groups, int tile) {
-    int lo = 0, hi = groups - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (t.tiles[mid + 1] > tile) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
-constexpr int kStages = 4;
 constexpr int kTileI = 128, kTileJ = 256;
 constexpr int kRowBytes = 128;                    // a stage's extent along a swizzled row
 constexpr int kABytes = kTileI * kRowBytes;       // 16 KiB a stage
-constexpr int kBBytes = kTileJ * kRowBytes;       // 32 KiB a stage
-constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBoxJ = 32;                         // rows of a K-major box of B
 constexpr int kBoxBytes = 64 * kRowBytes;         // MN-major box: 64 elements by 64 k
-constexpr int kMaxSplits = 16;
-constexpr int kThreads = 192;
-constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+constexpr int kWriters = 8;                       // warps that write accumulators out
+constexpr int kThreads = 64 + 32 * kWriters;
+constexpr int kSlotFloats = kTileI * kTileJ;      // one partial accumulator
+constexpr int kWidths = 8;                        // row-tile widths to choose from: 32, 64, ... 256
+
+// A CTA's share of B is half a pair's tile: two more stages fit.
+template <int CG>
+struct Ring {
+    static constexpr int kBBytes = kTileJ / CG * kRowBytes;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = CG == 1 ? 4 : 6;
+    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+};
 
 struct TcParams {
     CUtensorMap a, b;
     __nv_bfloat16 *out;
     const float *x_scales, *w_scales;
     const int64_t *begin, *count;
-    float *partial;       // gridDim.x accumulators of kTileJ x kTileI
-    unsigned *arrived;    // gridDim.x, zero between launches
+    float *partial;       // two accumulators a CTA
+    unsigned *arrived;    // two counters a CTA, zero between launches
     size_t ldy;
     long long rows;
     int groups, ni, n, k;
+    int wide;             // rows of out start on 16-byte boundaries
     unsigned long long *err;
 };
 
+// The launch's tiles, found from the groups by every CTA.
+struct Plan {
+    int tiles[kMaxGroups + 1];           // tiles before group g
+    long long blocks[kMaxGroups + 1];    // K blocks before group g, at least one a tile
+    int begin[kMaxGroups];
+    int count[kMaxGroups];
+    int down[kWidths];                   // row tiles of each width
+    int width;                           // of a row tile
+    int whole;                           // tiles that go round in whole waves
+    int runs;                            // CTAs that share the others
+    long long first, left;               // K blocks before the others, and of them
+    int bad;
+};
+
+// The group whose entry of a running total includes `at` (groups that add
+// nothing are skipped).
+template <typename T>
+__device__ __forceinline__ int group_of(const T *before, int groups, T at) {
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid + 1] > at) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// K blocks of one of group g's tiles; an empty sum counts as one.
+template <int MODE, int BK>
+__device__ __forceinline__ int tile_blocks(const TcParams &p, int count) {
+    return max(1, ((MODE == kGroupedGrad ? count : p.k) + BK - 1) / BK);
+}
+
+// Cost of a K block at a row-tile width, in clocks of an SM: the products, or
+// the fill of shared memory from L2 (measured: 47 bytes a clock).
+template <int CG>
+__device__ __forceinline__ float block_clocks(int width) {
+    return fmaxf(2.f * width, (kABytes + (float)(width * kRowBytes / CG)) / 47.f);
+}
+
+// A run's join costs about this many K blocks of time.
+constexpr int kJoinBlocks = 12;
+
+// Read and check the groups and lay out the tiles.  Every thread of the block
+// calls it; false if a group lies outside the rows or the groups hold more
+// rows than there are (so some overlap).
+template <int MODE, int BK, int CG>
+__device__ bool make_plan(Plan &t, const TcParams &p, int i_tiles, int ctas) {
+    if (threadIdx.x < kWidths) t.down[threadIdx.x] = 0;
+    if (threadIdx.x == 0) t.bad = 0;
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
+        const long long b = p.begin[g], c = p.count[g];
+        // c > rows first: b + c does not overflow
+        const bool bad = c < 0 || b < 0 || c > p.rows || b > p.rows - c;
+        if (bad) t.bad = 1;
+        t.begin[g] = (int)b;
+        t.count[g] = (int)c;
+        if (!bad) {
+            const int j = MODE == kGroupedGrad ? p.n : (int)c;
+#pragma unroll
+            for (int w = 0; w < kWidths; ++w) atomicAdd(&t.down[w], (j + 32 * w + 31) / (32 * w + 32));
+        }
+    }
+    __syncthreads();
+    if (t.bad) return false;
+    if (threadIdx.x < 32) {
+        // the width that costs least, the wider of two that cost the same
+        const int lane = threadIdx.x;
+        float cost = 3.4e38f;
+        if (lane < kWidths) {
+            const int w = 32 * lane + 32;
+            const float tiles = (float)t.down[lane] * i_tiles;
+            const float blocks = MODE == kGroupedGrad
+                                     ? fmaxf(1.f, (float)p.rows / (BK * (float)p.groups))
+                                     : (float)((p.k + BK - 1) / BK);
+            const float even = tiles / ctas, waves = ceilf(even);
+            cost = fminf(waves * blocks, even * blocks + kJoinBlocks) * block_clocks<CG>(w) + 12.f * w;
+        }
+        int width = 32 * lane + 32;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+            const int w = __shfl_xor_sync(0xffffffffu, width, o);
+            if (c < cost || (c == cost && w > width)) {
+                cost = c;
+                width = w;
+            }
+        }
+        int tiles = 0;
+        long long blocks = 0, held = 0;
+        for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            const int g = g0 + lane;
+            const int c = g < p.groups ? t.count[g] : 0;
+            int v = g < p.groups ? ((MODE == kGroupedGrad ? p.n : c) + width - 1) / width * i_tiles : 0;
+            long long k = (long long)v * tile_blocks<MODE, BK>(p, c);
+            held += c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                const long long q = __shfl_up_sync(0xffffffffu, k, o);
+                if (lane >= o) {
+                    v += u;
+                    k += q;
+                }
+            }
+            if (g < p.groups) {
+                t.tiles[g + 1] = tiles + v;
+                t.blocks[g + 1] = blocks + k;
+            }
+            tiles += __shfl_sync(0xffffffffu, v, 31);
+            blocks += __shfl_sync(0xffffffffu, k, 31);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) held += __shfl_xor_sync(0xffffffffu, held, o);
+        __syncwarp();
+        if (lane == 0) {
+            t.tiles[0] = 0;
+            t.blocks[0] = 0;
+            t.width = width;
+            if (held > p.rows) t.bad = 1;
+            // Runs of K blocks for what does not fill whole waves, where the time
+            // that idle CTAs would waste is more than a join's.
+            const int waves = (tiles + ctas - 1) / ctas;
+            int whole = tiles;
+            if (!t.bad && tiles % ctas != 0) {
+                const long long wasted = (long long)waves * ctas - tiles;
+                if (wasted * (blocks / tiles) >= (long long)kJoinBlocks * ctas)
+                    whole = max(0, waves - 2) * ctas;
+            }
+            t.whole = whole;
+            long long first = blocks;
+            if (whole < tiles) {
+                const int g = group_of(t.tiles, p.groups, whole);
+                first = t.blocks[g] + (long long)(whole - t.tiles[g]) *
+                                          tile_blocks<MODE, BK>(p, t.count[g]);
+            }
+            t.first = first;
+            t.left = blocks - first;
+            // at least four blocks a run
+            t.runs = (int)max(1ll, min((long long)ctas, t.left / 4));
+        }
+    }
+    __syncthreads();
+    return !t.bad;
+}
+
 struct TcShared {
-    GroupTable table;
+    Plan plan;
     snac::Ctl ctl;
-    uint64_t full[kStages], empty[kStages];   // stage loaded; stage consumed
-    uint64_t done[2], free[2];                // accumulator complete; accumulator read
+    uint64_t full[6], empty[6];   // stage loaded (for the leader, in both CTAs); consumed
+    uint64_t done[2], free[2];    // accumulator complete; accumulator read
     uint64_t drain;
     uint32_t tmem;
     int last;
+    alignas(16) __nv_bfloat16 turn[kWriters][16][32];   // 16 rows of 32 channels a warp
 };
 
-// One CTA's share of a tile: blocks [kb0, kb1) of the K axis.
+// What a CTA (or pair) does next: K blocks [kb0, kb1) of a tile.
 struct Unit {
-    int g, i0, j0, nj;   // nj: valid columns, up to kTileJ
+    int g, i0, j0, nj;   // nj: valid columns, up to the width
     int row0;            // first row of the group
     int nk;              // K extent
-    int kb0, kb1;
-    int tile, split;
+    int kb0, kb1;        // kb0 == kb1: the sum over nothing
+    int tile;
+    int c0, c1;          // the tile's runs, first and last; equal where nobody shares it
 };
 
-template <int MODE, int BK>
-__device__ __forceinline__ Unit unit_at(const TcParams &p, const GroupTable &t, int u, int splits,
-                                        int i_tiles) {
-    Unit q;
-    q.tile = u / splits;
-    q.split = u - q.tile * splits;
-    q.g = group_of(t, p.groups, q.tile);
-    const int local = q.tile - t.tiles[q.g];
-    const int jt = local / i_tiles;
-    q.i0 = (local - jt * i_tiles) * kTileI;
-    q.j0 = jt * kTileJ;
-    q.row0 = t.begin[q.g];
-    q.nj = min(kTileJ, (MODE == kGroupedGrad ? p.n : t.count[q.g]) - q.j0);
-    q.nk = MODE == kGroupedGrad ? t.count[q.g] : p.k;
-    const int blocks = (q.nk + BK - 1) / BK;
-    q.kb0 = (int)((long long)blocks * q.split / splits);
-    q.kb1 = (int)((long long)blocks * (q.split + 1) / splits);
-    return q;
+__device__ __forceinline__ long long run_begin(const Plan &t, int c) { return t.left * c / t.runs; }
+
+__device__ __forceinline__ int run_of(const Plan &t, long long block) {
+    return (int)(((block + 1) * t.runs - 1) / t.left);
 }
 
-template <int MODE, bool BF16>
+// Walks the units of one CTA (or pair) `c` of `ctas`.
+template <int MODE, int BK, int CG>
+struct Walk {
+    const TcParams &p;
+    const Plan &t;
+    int i_tiles, c, ctas;
+    int tile;             // next whole tile
+    long long at, end;    // the run's blocks still to do
+    __device__ Walk(const TcParams &p, const Plan &t, int i_tiles, int c, int ctas)
+        : p(p), t(t), i_tiles(i_tiles), c(c), ctas(ctas), tile(c) {
+        at = end = 0;
+        if (t.left > 0 && c < t.runs) {
+            at = run_begin(t, c);
+            end = run_begin(t, c + 1);
+        }
+    }
+    __device__ bool next(Unit &q) {
+        if (tile < t.whole) {
+            q.tile = tile;
+            tile += ctas;
+            q.g = group_of(t.tiles, p.groups, q.tile);
+            place(q);
+            q.kb0 = 0;
+            q.kb1 = (q.nk + BK - 1) / BK;
+            q.c0 = q.c1 = c;
+            return true;
+        }
+        if (at >= end) return false;
+        const long long block = t.first + at;
+        q.g = group_of(t.blocks, p.groups, block);
+        const int each = tile_blocks<MODE, BK>(p, t.count[q.g]);
+        const int local = (int)((block - t.blocks[q.g]) / each);
+        q.tile = t.tiles[q.g] + local;
+        const long long begin = t.blocks[q.g] + (long long)local * each - t.first;
+        place(q);
+        q.kb0 = (int)(at - begin);
+        q.kb1 = (int)(min(end, begin + each) - begin);
+        at = begin + q.kb1;
+        q.c0 = run_of(t, begin);
+        q.c1 = run_of(t, begin + each - 1);
+        if (q.nk == 0) q.kb1 = q.kb0;
+        return true;
+    }
+    // Where run r's partial of the tile with K block `begin` lies: a run has at
+    // most two, of the tile it begins in and of the one it ends in.
+    __device__ int slot(int r, long long begin) const {
+        return 2 * r + (run_begin(t, r) >= begin ? 0 : 1);
+    }
+    __device__ long long tile_begin(const Unit &q) const {
+        return t.blocks[q.g] - t.first +
+               (long long)(q.tile - t.tiles[q.g]) * tile_blocks<MODE, BK>(p, t.count[q.g]);
+    }
+    __device__ void place(Unit &q) const {
+        const int local = q.tile - t.tiles[q.g];
+        const int jt = local / i_tiles;
+        q.i0 = (local - jt * i_tiles) * (kTileI * CG);
+        q.j0 = jt * t.width;
+        q.row0 = t.begin[q.g];
+        q.nj = min(t.width, (MODE == kGroupedGrad ? p.n : t.count[q.g]) - q.j0);
+        q.nk = MODE == kGroupedGrad ? t.count[q.g] : p.k;
+    }
+};
+
+// Columns of the instruction for nj valid ones: what its shape allows.
+template <int CG>
+__device__ __forceinline__ int columns_of(int nj) {
+    return (nj + 16 * CG - 1) / (16 * CG) * (16 * CG);
+}
+
+// Wait for a barrier's phase, two seconds at most; `abortable`: give up as soon
+// as another role of the CTA has.
+__device__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile snac::Ctl *ctl,
+                             unsigned long long *err, bool abortable) {
+    uint64_t t0 = 0;   // the timer is slow to read: not before some 60 tries
+    for (uint32_t it = 1;; ++it) {
+        if (atom::mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (abortable && ctl->abort) return false;
+            const uint64_t now = atom::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > snac::kRingWaitNs) {
+                snac::record_error(err, PURLIN_ERR_TIMEOUT, snac::kSiteGroupedWait, blockIdx.x);
+                ctl->abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+template <int MODE, bool BF16, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_tc_kernel(const __grid_constant__ TcParams p) {
+    using R = Ring<CG>;
     constexpr int BK = BF16 ? 64 : 128;        // K elements a stage
     constexpr int KSTEP = BF16 ? 16 : 32;      // K elements an instruction
     constexpr bool A_MN = MODE != kGroupedNK, B_MN = MODE == kGroupedGrad;
@@ -179,163 +343,164 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
     __shared__ TcShared s;
     const uint32_t stage0 = (atom::smem_u32(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1);   // in the pair; 0 leads
+    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
 
     if (warp == 0 && lane == 0) {
         tensor::prefetch_map(&p.a);
         tensor::prefetch_map(&p.b);
-        for (int i = 0; i < kStages; ++i) {
-            atom::mbar_init(&s.full[i], 1);
+        for (int i = 0; i < R::kStages; ++i) {
+            atom::mbar_init(&s.full[i], CG == 2 && rank == 0 ? 2 : 1);
             atom::mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             atom::mbar_init(&s.done[i], 1);
-            atom::mbar_init(&s.free[i], 4);
+            atom::mbar_init(&s.free[i], kWriters * CG);
         }
         atom::mbar_init(&s.drain, 1);
         atom::mbar_init_fence();
         s.ctl.abort = 0;
     }
-    const int i_tiles = (p.ni + kTileI - 1) / kTileI;
-    const bool ok = read_groups(s.table, p.begin, p.count, p.groups, p.rows, [&](int c) {
-        return ((MODE == kGroupedGrad ? p.n : c) + kTileJ - 1) / kTileJ * i_tiles;
-    });
-    if (!ok) {
+    const int i_tiles = (p.ni + kTileI * CG - 1) / (kTileI * CG);
+    if (!make_plan<MODE, BK, CG>(s.plan, p, i_tiles, groups)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             snac::record_error(p.err, PURLIN_ERR_INVALID_ARG, snac::kSiteGroups, 0);
         return;
     }
-    const int tiles = s.table.tiles[p.groups];
-    // Splits of K: as many as the grid has CTAs for, at least four blocks each.
-    const int blocks = ((MODE == kGroupedGrad ? s.table.most : p.k) + BK - 1) / BK;
-    const int splits =
-        tiles == 0 ? 1
-                   : max(1, min(min((int)gridDim.x / tiles, kMaxSplits), blocks / 4));
-    const int units = tiles * splits;
-    if ((int)blockIdx.x >= units) return;
+    const Plan &plan = s.plan;
+    if (group >= plan.whole && (plan.left == 0 || group >= plan.runs)) return;   // nothing to do
 
-    if (warp == 1) tensor::tmem_alloc(&s.tmem, 512);
+    if (warp == 1) tensor::tmem_alloc<CG>(&s.tmem, 512);
     tensor::fence_before_sync();
-    __syncthreads();
+    tensor::sync_ctas<CG>();
     tensor::fence_after_sync();
     const uint32_t tmem = s.tmem;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return snac::ring_wait(bar, parity, &s.ctl, p.err, snac::kSiteGroupedWait, true);
+        return bounded_wait(bar, parity, &s.ctl, p.err, true);
     };
     // one answer for the warp, whichever lanes saw the wait expire
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
     };
-    uint32_t filled = 0;   // stages that warp 0's lane 0 has filled
+    uint32_t filled = 0;   // stages that this thread has filled
+    Walk<MODE, BK, CG> walk(p, plan, i_tiles, group, groups);
+    Unit q;
 
-    if (warp == 0) {
-        // ---- load
-        if (lane == 0) {
-            uint32_t &it = filled;
+    if (warp < 2) {
+        // One thread loads, one multiplies: nothing but them on a stage's path.
+        if (!tensor::elect()) {
+        } else if (warp == 0) {
+            // ---- load
             bool run = true;
-            for (int u = blockIdx.x; u < units && run; u += gridDim.x) {
-                const Unit q = unit_at<MODE, BK>(p, s.table, u, splits, i_tiles);
-                const int boxes = B_MN ? (q.nj + 63) / 64 : (q.nj + kBoxJ - 1) / kBoxJ;
+            while (run && walk.next(q)) {
+                const int half = columns_of<CG>(q.nj) / CG;
+                const int mine = CG == 1 ? q.nj : half;   // columns of this CTA's share
+                const int boxes = B_MN ? (mine + 63) / 64 : (mine + kBoxJ - 1) / kBoxJ;
                 const uint32_t bytes = kABytes + boxes * (B_MN ? kBoxBytes : kBoxJ * kRowBytes);
-                for (int kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-                    const uint32_t st = it % kStages;
-                    if (!wait(&s.empty[st], ((it / kStages) & 1) ^ 1)) {
+                const int i0 = q.i0 + rank * kTileI, j0 = q.j0 + rank * half;
+                for (int kb = q.kb0; kb < q.kb1; ++kb, ++filled) {
+                    const uint32_t st = filled % R::kStages;
+                    if (!wait(&s.empty[st], ((filled / R::kStages) & 1) ^ 1)) {
                         run = false;
                         break;
                     }
                     const uint32_t bar = atom::smem_u32(&s.full[st]);
-                    const uint32_t a = stage0 + st * kStageBytes, b = a + kABytes;
+                    const uint32_t a = stage0 + st * R::kStageBytes, b = a + kABytes;
                     atom::mbar_arrive_expect_tx(&s.full[st], bytes);
                     if constexpr (MODE == kGroupedNK) {
-                        tensor::load_box_3d(a, &p.a, kb * BK, q.i0, q.g, bar);
+                        tensor::load_box_3d(a, &p.a, kb * BK, i0, q.g, bar);
                     } else if constexpr (MODE == kGroupedKN) {
+#pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            tensor::load_box_3d(a + h * kBoxBytes, &p.a, q.i0 + 64 * h, kb * BK,
-                                                q.g, bar);
+                            tensor::load_box_3d(a + h * kBoxBytes, &p.a, i0 + 64 * h, kb * BK, q.g,
+                                                bar);
                     } else {
+#pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            tensor::load_box_2d(a + h * kBoxBytes, &p.a, q.i0 + 64 * h,
+                            tensor::load_box_2d(a + h * kBoxBytes, &p.a, i0 + 64 * h,
                                                 q.row0 + kb * BK, bar);
                     }
                     for (int h = 0; h < boxes; ++h) {
                         if constexpr (B_MN)
-                            tensor::load_box_2d(b + h * kBoxBytes, &p.b, q.j0 + 64 * h,
+                            tensor::load_box_2d(b + h * kBoxBytes, &p.b, j0 + 64 * h,
                                                 q.row0 + kb * BK, bar);
                         else
                             tensor::load_box_2d(b + h * kBoxJ * kRowBytes, &p.b, kb * BK,
-                                                q.row0 + q.j0 + kBoxJ * h, bar);
+                                                q.row0 + j0 + kBoxJ * h, bar);
                     }
                 }
             }
-        }
-    } else if (warp == 1) {
-        // ---- multiply
-        uint32_t it = 0, acc = 0;
-        bool run = true;
-        for (int u = blockIdx.x; u < units && run; u += gridDim.x) {
-            const Unit q = unit_at<MODE, BK>(p, s.table, u, splits, i_tiles);
-            if (q.kb0 == q.kb1) continue;   // an empty group, or a split with no block
-            const uint32_t buf = acc & 1;
-            if (!wait_warp(&s.free[buf], ((acc >> 1) & 1) ^ 1)) break;
-            ++acc;
-            tensor::fence_after_sync();
-            const uint32_t d = tmem + buf * kTileJ;
-            const uint32_t idesc =
-                tensor::instr_desc(BF16 ? 1 : 0, A_MN, B_MN, kTileI, (q.nj + 15) & ~15);
-            for (int kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-                const uint32_t st = it % kStages;
-                if (!wait_warp(&s.full[st], (it / kStages) & 1)) {
-                    run = false;
-                    break;
+        } else {
+            // ---- multiply; the pair's other CTA passes on that its stages are loaded
+            uint32_t it = 0, acc = 0;
+            bool run = true;
+            while (run && walk.next(q)) {
+                if (q.kb0 == q.kb1) continue;   // a sum over nothing
+                const uint32_t buf = acc & 1;
+                if (rank == 0) {
+                    if (!wait(&s.free[buf], ((acc >> 1) & 1) ^ 1)) break;
+                    tensor::fence_after_sync();
                 }
-                tensor::fence_after_sync();
-                const uint32_t a = stage0 + st * kStageBytes, b = a + kABytes;
-                const int left = min(BK, q.nk - kb * BK);
-                const int steps = (left + KSTEP - 1) / KSTEP;
-                if constexpr (MODE == kGroupedGrad) {
-                    // rows past the group's end inside the last instruction's 16
-                    if (left < steps * KSTEP) {
-                        const int quads = (steps * KSTEP - left) * (kRowBytes / 16);
-                        const int boxes = 2 + (q.nj + 63) / 64;
-                        for (int e = lane; e < quads * boxes; e += 32) {
-                            const int box = e / quads, at = e - box * quads;
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             a + box * kBoxBytes + left * kRowBytes + at * 16),
-                                         "r"(0)
-                                         : "memory");
-                        }
-                        tensor::fence_async_shared();
-                        __syncwarp();
+                ++acc;
+                const uint32_t d = tmem + buf * kTileJ;
+                const int columns = columns_of<CG>(q.nj);
+                const uint32_t idesc =
+                    tensor::instr_desc(BF16 ? 1 : 0, A_MN, B_MN, kTileI * CG, columns);
+                for (int kb = q.kb0; kb < q.kb1; ++kb, ++it) {
+                    const uint32_t st = it % R::kStages;
+                    if (!wait(&s.full[st], (it / R::kStages) & 1)) {
+                        run = false;
+                        break;
                     }
-                }
-                if (lane == 0) {
+                    const uint32_t a = stage0 + st * R::kStageBytes, b = a + kABytes;
+                    const int left = min(BK, q.nk - kb * BK);
+                    const int steps = (left + KSTEP - 1) / KSTEP;
+                    const bool cut = MODE == kGroupedGrad && left < steps * KSTEP;
+                    if (cut) {
+                        // rows past the group's end inside the last instruction's 16
+                        const int boxes = 2 + (columns / CG + 63) / 64;
+                        for (int box = 0; box < boxes; ++box)
+                            for (int at = left * kRowBytes; at < steps * KSTEP * kRowBytes; at += 16)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 a + box * kBoxBytes + at),
+                                             "r"(0)
+                                             : "memory");
+                        tensor::fence_async_shared();
+                    }
+                    if (rank != 0) {
+                        tensor::arrive_cluster(tensor::in_cta(atom::smem_u32(&s.full[st]), 0), cut);
+                        continue;
+                    }
+                    tensor::fence_after_sync();
                     const uint64_t da = tensor::operand_desc(a, kBoxBytes);
                     const uint64_t db = tensor::operand_desc(b, kBoxBytes);
-                    for (int k = 0; k < steps; ++k) {
-                        // K-major: 32 bytes on along the row; MN-major: 16 rows on
-                        const uint64_t oa = (uint64_t)k * (A_MN ? 16 * kRowBytes : 32) >> 4;
-                        const uint64_t ob = (uint64_t)k * (B_MN ? 16 * kRowBytes : 32) >> 4;
-                        tensor::mma<BF16>(d, da + oa, db + ob, idesc, kb > q.kb0 || k > 0);
-                    }
-                    tensor::commit(atom::smem_u32(&s.empty[st]));
-                    if (kb + 1 == q.kb1) tensor::commit(atom::smem_u32(&s.done[buf]));
+                    // K-major: 32 bytes on along the row; MN-major: 16 rows on
+                    constexpr uint64_t kNextA = (A_MN ? 16 * kRowBytes : 32) >> 4;
+                    constexpr uint64_t kNextB = (B_MN ? 16 * kRowBytes : 32) >> 4;
+#pragma unroll
+                    for (int k = 0; k < BK / KSTEP; ++k)
+                        if (k < steps)
+                            tensor::mma<BF16, CG>(d, da + k * kNextA, db + k * kNextB, idesc,
+                                                  kb > q.kb0 || k > 0);
+                    tensor::commit<CG>(atom::smem_u32(&s.empty[st]));
+                    if (kb + 1 == q.kb1) tensor::commit<CG>(atom::smem_u32(&s.done[buf]));
                 }
-                __syncwarp();
             }
         }
     } else {
-        // ---- write out; warp w reads lanes 32 (w % 4) on of the accumulator
-        const int quarter = warp & 3;
+        // ---- write out; warp w reads lanes 32 (w % 4) on of the accumulator, and
+        // every other 32 columns of them
+        const int quarter = warp & 3, c_first = 32 * ((warp - 2) >> 2);
+        constexpr int kColStep = 32 * kWriters / 4;
         uint32_t acc = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            const Unit q = unit_at<MODE, BK>(p, s.table, u, splits, i_tiles);
-            const int i = q.i0 + quarter * 32 + lane;
-            const bool live = i < p.ni;
+        bool dead = false;   // a wait expired: walk on, for the barriers of shared tiles
+        while (walk.next(q)) {
+            const int i = q.i0 + rank * kTileI + quarter * 32 + lane;
+            const bool live = i < p.ni, shared = q.c0 != q.c1;
             const bool empty = q.kb0 == q.kb1;
             const uint32_t buf = acc & 1;
-            bool good = true;
-            if (!empty) {
-                good = wait_warp(&s.done[buf], (acc >> 1) & 1);
-                if (!good && splits == 1) break;   // with splits: on to the barriers below
+            if (!empty && !dead) {
+                dead = !wait_warp(&s.done[buf], (acc >> 1) & 1);
                 ++acc;
                 tensor::fence_after_sync();
             }
@@ -344,82 +509,154 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
             __nv_bfloat16 *out = p.out + row * p.ldy + i;
             float ws = 1.f;
             if constexpr (!BF16) ws = live ? p.w_scales[(size_t)q.g * p.n + i] : 0.f;
-            float *mine = p.partial + (size_t)u * kTileJ * kTileI + quarter * 32 + lane;
-            auto put = [&](int j, float v, float xs) {
-                if constexpr (!BF16) v = v * xs * ws;
-                out[(size_t)j * p.ldy] = __float2bfloat16_rn(v);
-            };
-            for (int c = 0; c < q.nj && good; c += 32) {
-                uint32_t v[32];
+            // 32 columns of the accumulator from column c on
+            auto fetch = [&](int c, float (&v)[32]) {
                 __syncwarp();
                 if (!empty) {
-                    tensor::tmem_load32(tmem + buf * kTileJ + c + ((uint32_t)quarter << 21), v);
+                    uint32_t r[32];
+                    tensor::tmem_load32(tmem + buf * kTileJ + c + ((uint32_t)quarter << 21), r);
                     tensor::tmem_wait_loads();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = 0;
+                    for (int x = 0; x < 32; ++x) v[x] = 0.f;
                 }
+            };
+            // Rows of out are rows of the accumulator's columns: sixteen at a time
+            // turn in shared memory, so that a store is 16 bytes and not 2 (an
+            // epilogue of 2-byte stores took 10 us a tile, five times this one).
+            auto put = [&](int c, float (&v)[32]) {
                 const int width = min(32, q.nj - c);
-                if (splits == 1) {
-                    float xs = 0.f;
-                    if constexpr (!BF16)
-                        if (lane < width) xs = p.x_scales[row + c + lane];
+                if constexpr (!BF16) {
+                    const float xs = lane < width ? p.x_scales[row + c + lane] : 0.f;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) v[x] = v[x] * __shfl_sync(0xffffffffu, xs, x) * ws;
+                }
+                if (!p.wide) {
+                    __nv_bfloat16 *to = out + (size_t)c * p.ldy;
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
-                        const float sx = BF16 ? 1.f : __shfl_sync(0xffffffffu, xs, x);
-                        if (x < width && live) put(c + x, __uint_as_float(v[x]), sx);
+                        if (x < width && live) *to = __float2bfloat16_rn(v[x]);
+                        to += p.ldy;
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (x < width) __stcg(mine + (size_t)(c + x) * kTileI, __uint_as_float(v[x]));
+                    return;
                 }
+                __nv_bfloat16(&turn)[16][32] = s.turn[warp - 2];
+                const int ch = (lane & 3) * 8, room = p.ni - (i - lane) - ch;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (16 * h >= width) break;
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) turn[x][lane] = __float2bfloat16_rn(v[16 * h + x]);
+                    __syncwarp();
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int r = 8 * t + (lane >> 2), j = c + 16 * h + r;
+                        if (j >= q.nj || room <= 0) continue;
+                        __nv_bfloat16 *to = out - lane + ch + (size_t)j * p.ldy;
+                        if (room >= 8) {
+                            *reinterpret_cast<uint4 *>(to) =
+                                *reinterpret_cast<const uint4 *>(&turn[r][ch]);
+                        } else {
+                            for (int e = 0; e < room; ++e) to[e] = turn[r][ch + e];
+                        }
+                    }
+                }
+            };
+            float v[32];
+            if (!shared) {
+                for (int c = c_first; c < q.nj && !dead; c += kColStep) {
+                    fetch(c, v);
+                    put(c, v);
+                }
+            } else {
+                // slot: [column / 4][lane of 128][4 columns]
+                const long long begin = walk.tile_begin(q);
+                auto slot_of = [&](int r) {
+                    return reinterpret_cast<float4 *>(p.partial) +
+                           ((size_t)walk.slot(r, begin) * CG + rank) * (kSlotFloats / 4) +
+                           quarter * 32 + lane;
+                };
+                float4 *mine = slot_of(group);
+                for (int c = c_first; c < q.nj && !dead; c += kColStep) {
+                    fetch(c, v);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (c + 4 * x < q.nj)
+                            __stcg(mine + (size_t)(c / 4 + x) * kTileI,
+                                   make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
+                }
+                // the last of the tile's CTAs adds the accumulators in K order
+                __threadfence();
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
+                if (warp == 2 && lane == 0) {
+                    unsigned *n = p.arrived + (size_t)(q.tile - plan.whole) * CG + rank;
+                    s.last = atomicAdd(n, 1u) == (unsigned)(q.c1 - q.c0);
+                    if (s.last) *n = 0;
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
+                if (s.last && !dead) {
+                    __threadfence();
+                    for (int c = c_first; c < q.nj; c += kColStep) {
+                        float sum[32];
+                        fetch(c, v);   // this CTA's own
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) sum[x] = 0.f;
+                        for (int r = q.c0; r <= q.c1; ++r) {
+                            if (r == group) {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) sum[x] += v[x];
+                                continue;
+                            }
+                            const float4 *from = slot_of(r);
+                            float4 u[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                u[x] = c + 4 * x < q.nj ? __ldcg(from + (size_t)(c / 4 + x) * kTileI)
+                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                sum[4 * x] += u[x].x;
+                                sum[4 * x + 1] += u[x].y;
+                                sum[4 * x + 2] += u[x].z;
+                                sum[4 * x + 3] += u[x].w;
+                            }
+                        }
+                        put(c, sum);
+                    }
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");   // s.last is free again
             }
-            if (!empty) {
+            if (!empty && !dead) {
                 tensor::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) atom::mbar_arrive(&s.free[buf]);
-            }
-            if (splits > 1) {
-                // the last of the tile's CTAs adds the accumulators in split order
-                __threadfence();
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (warp == 2 && lane == 0) {
-                    const unsigned before = atomicAdd(&p.arrived[q.tile], 1u);
-                    s.last = before + 1 == (unsigned)splits;
-                    if (s.last) p.arrived[q.tile] = 0;
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (s.last && live && good) {
-                    __threadfence();
-                    const float *all = p.partial + (size_t)q.tile * splits * kTileJ * kTileI +
-                                       quarter * 32 + lane;
-                    for (int j = 0; j < q.nj; ++j) {
-                        float v = 0.f;
-                        for (int k = 0; k < splits; ++k)
-                            v += __ldcg(all + ((size_t)k * kTileJ + j) * kTileI);
-                        put(j, v, BF16 ? 1.f : p.x_scales[row + j]);
-                    }
+                if (lane == 0) {
+                    const uint32_t bar = atom::smem_u32(&s.free[buf]);
+                    if constexpr (CG == 1) atom::mbar_arrive(&s.free[buf]);
+                    else tensor::arrive_cluster(tensor::in_cta(bar, 0), false);
                 }
             }
         }
     }
     tensor::fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    tensor::sync_ctas<CG>();
     tensor::fence_after_sync();
     if (s.ctl.abort) {
         // a wait expired: let the copies and products in flight end before the exit
-        if (warp == 0 && lane == 0)
-            for (uint32_t o = filled > kStages ? filled - kStages : 0; o < filled; ++o)
-                snac::ring_wait(&s.full[o % kStages], (o / kStages) & 1, &s.ctl, p.err,
-                                snac::kSiteGroupedWait, false);
-        if (warp == 1) {
-            if (lane == 0) tensor::commit(atom::smem_u32(&s.drain));
-            snac::ring_wait(&s.drain, 0, &s.ctl, p.err, snac::kSiteGroupedWait, false);
+        if (warp == 0)
+            for (uint32_t o = filled > R::kStages ? filled - R::kStages : 0; o < filled; ++o)
+                bounded_wait(&s.full[o % R::kStages], (o / R::kStages) & 1, &s.ctl, p.err, false);
+        if (warp == 1 && rank == 0) {
+            if (tensor::elect()) tensor::commit<CG>(atom::smem_u32(&s.drain));
+            bounded_wait(&s.drain, 0, &s.ctl, p.err, false);
         }
-        __syncthreads();
+        __syncwarp();
     }
-    if (warp == 1) tensor::tmem_free(tmem, 512);
+    tensor::sync_ctas<CG>();
+    if (warp == 1) tensor::tmem_free<CG>(tmem, 512);
 }
 
 // ------------------------------------------------------------------- host --
@@ -459,18 +696,42 @@ bool make_map(CUtensorMap *m, const void *p, int dtype, int rank, size_t d0, siz
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool BF16>
-cudaError_t launch_tc(const GroupedArgs &a, TcParams &p) {
+template <int MODE, bool BF16, int CG>
+cudaError_t launch_tc(const GroupedArgs &a, const TcParams &p) {
+    constexpr uint32_t smem = Ring<CG>::kSmem;
     static const cudaError_t ready = cudaFuncSetAttribute(
-        grouped_tc_kernel<MODE, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        grouped_tc_kernel<MODE, BF16, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ready != cudaSuccess) return ready;
-    grouped_tc_kernel<MODE, BF16><<<a.sms, kThreads, kSmem, a.stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(a.sms / CG * CG));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = a.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {CG, 1, 1};
+    c.attrs = at;
+    c.numAttrs = CG == 1 ? 0 : 1;
+    return cudaLaunchKernelEx(&c, grouped_tc_kernel<MODE, BF16, CG>, p);
+}
+
+template <int MODE, bool BF16>
+cudaError_t launch_mode(const GroupedArgs &a, const TcParams &p) {
+    // A pair halves what each CTA loads of B, and its tiles are twice as wide: it
+    // pays where K is long and the groups fill its tiles.  16384 x 7168 x 2048 over 8
+    // groups: 323 us against 349 alone; K = 576 (5784 rows, 3 groups): 22.0 against
+    // 18.5; 10066 rows over 14 groups, 384 channels, forward K and backward: 80 against
+    // 74.  Channels that fill a wider tile badly stay with single CTAs.
+    const size_t per_group = a.rows / (size_t)a.groups;
+    const size_t kext = MODE == kGroupedGrad ? per_group : a.k;
+    const size_t wide = ((size_t)p.ni + 255) / 256 * 2, narrow = ((size_t)p.ni + 127) / 128;
+    const bool pair = kext >= 1024 && per_group >= 512 && 8 * wide <= 9 * narrow && a.sms >= 2;
+    return pair ? launch_tc<MODE, BF16, 2>(a, p) : launch_tc<MODE, BF16, 1>(a, p);
 }
 
 }  // namespace
 
-size_t grouped_workspace(int sms) { return (size_t)sms * kTileI * kTileJ * sizeof(float); }
+size_t grouped_workspace(int sms) { return 2 * (size_t)sms * kSlotFloats * sizeof(float); }
 
 cudaError_t launch_grouped(const GroupedArgs &a) {
     TcParams p;
@@ -499,11 +760,12 @@ cudaError_t launch_grouped(const GroupedArgs &a) {
     p.ni = (int)(a.mode == kGroupedGrad ? a.k : a.n);
     p.n = (int)a.n;
     p.k = (int)a.k;
+    p.wide = ((reinterpret_cast<uintptr_t>(a.y) | (a.ldy * sizeof(__nv_bfloat16))) & 15u) == 0;
     p.err = a.err;
-    if (a.dtype == PURLIN_E4M3) return launch_tc<kGroupedNK, false>(a, p);
-    if (a.mode == kGroupedNK) return launch_tc<kGroupedNK, true>(a, p);
-    if (a.mode == kGroupedKN) return launch_tc<kGroupedKN, true>(a, p);
-    return launch_tc<kGroupedGrad, true>(a, p);
+    if (a.dtype == PURLIN_E4M3) return launch_mode<kGroupedNK, false>(a, p);
+    if (a.mode == kGroupedNK) return launch_mode<kGroupedNK, true>(a, p);
+    if (a.mode == kGroupedKN) return launch_mode<kGroupedKN, true>(a, p);
+    return launch_mode<kGroupedGrad, true>(a, p);
 }
 
 }  // namespace purlin

@@ -139,7 +139,7 @@ struct purlin_ctx {
     std::list<purlin::host::ChannelMem> channels;          // memory of packet channels
     purlin::host::WorkMem work;                 // the layer operators' partial results
     purlin::host::WorkMem *old_work = nullptr;  // outgrown, kept for captured graphs
-    unsigned *arrived = nullptr;                // kMaxSms counters of the grouped products' joins
+    unsigned *arrived = nullptr;                // kJoinCounters counters of the grouped products' joins
 };
 
 namespace purlin {

@@ -72,15 +72,15 @@ struct GroupedArgs {
     int dtype = 0;
     int sms = 0;
     float *partial = nullptr;       // grouped_workspace(sms) bytes
-    unsigned *arrived = nullptr;    // kMaxSms counters, zero between launches
+    unsigned *arrived = nullptr;    // kJoinCounters, zero between launches
     unsigned long long *err = nullptr;
     cudaStream_t stream = nullptr;
 };
 
 constexpr int kMaxGroups = PURLIN_MAX_GROUPS;
-constexpr int kMaxSms = 1024;
-constexpr size_t kGroupedMaxRowTile = 256;   // rows of a tile, channels of a tile
-constexpr size_t kGroupedTileChannels = 128;
+constexpr int kJoinCounters = 2048;          // two an SM
+constexpr size_t kGroupedRowTile = 32;       // the narrowest tile's rows, and its channels
+constexpr size_t kGroupedChannelTile = 128;
 
 size_t grouped_workspace(int sms);
 

@@ -15,7 +15,7 @@ using namespace purlin::host;
 
 namespace {
 
-constexpr size_t kMaxExtent = 0x7FFFFFFF;         // rows, columns: 32-bit coordinates
+constexpr size_t kMaxExtent = 0x7FFFF000;         // rows, columns: 32-bit coordinates, a tile past the end too
 constexpr size_t kMaxPitch = (size_t)1 << 35;     // elements
 
 int size_of(int dtype) { return dtype == PURLIN_F32 ? 4 : dtype == PURLIN_BF16 ? 2 : 1; }
@@ -59,8 +59,8 @@ bool bad_ld(size_t ld, size_t cols) { return ld < cols || ld > kMaxPitch; }
 // can be counted in 32 bits, and a weight matrix's pitch in the 40 that a
 // tensor map has.
 bool too_many_tiles(size_t channels, size_t tall, size_t each_group, int groups) {
-    const size_t across = channels / kGroupedTileChannels + 1;
-    const size_t down = tall / kGroupedMaxRowTile + each_group * (size_t)groups;
+    const size_t across = channels / kGroupedChannelTile + 1;
+    const size_t down = tall / kGroupedRowTile + each_group * (size_t)groups;
     return across * down > kMaxExtent / 2;
 }
 bool too_long(size_t rows, size_t ld, size_t es) {
@@ -342,7 +342,7 @@ purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy,
     if (overlap(mw, matrix(dy, rows, n, lddy, dtype)) ||
         overlap(mw, matrix(x, rows, k, ldx, dtype)))
         return PURLIN_ERR_ALIAS;
-    if (too_many_tiles(k, 0, n / kGroupedMaxRowTile + 1, groups)) return PURLIN_ERR_UNSUPPORTED;
+    if (too_many_tiles(k, 0, n / kGroupedRowTile + 1, groups)) return PURLIN_ERR_UNSUPPORTED;
     if (ctx == nullptr) return PURLIN_ERR_INVALID_ARG;
     if (rows == 0)
         return cudaMemset2DAsync(dw, lddw * 2, 0, k * 2, (size_t)groups * n, ctx->stream) ==

@@ -13,6 +13,18 @@
 namespace purlin {
 namespace tensor {
 
+// One thread of a converged warp, always the same one.  Instructions that take
+// their operands from uniform registers (TMA, tcgen05) are issued under it: under
+// a test of the lane's number the compiler cannot tell that one thread is active,
+// and the product of a K block took twice its time.
+__device__ __forceinline__ bool elect() {
+    uint32_t one = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.u32 %0, 1;\n\t}"
+        : "+r"(one));
+    return one != 0;
+}
+
 // ------------------------------------------------------------------- TMA --
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
@@ -43,20 +55,69 @@ __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// ---------------------------------------------------------- tensor memory --
+// -------------------------------------------------------------- CTA pairs --
 
-// Whole warp.  The column base is written to shared memory.
-__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     atom::smem_u32(dst)),
-                 "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+// The address, in the cluster's window, of what lies at `smem` in CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(uint32_t smem, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
 }
 
+// Arrive on a barrier of either CTA (an address of in_cta).  `published`: this
+// thread's warp wrote shared memory that the other CTA's products read.  Without
+// such writes the order within the CTA is enough: what the barrier guards was
+// written by TMA or read by tcgen05.ld, and a release at cluster scope on every
+// stage costs more than the stage (measured: twice the time of the whole product).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar, bool published) {
+    if (published)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                     : "memory");
+    else
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Every thread of the CTA, or of both CTAs of a pair.
+template <int CG>
+__device__ __forceinline__ void sync_ctas() {
+    if constexpr (CG == 1) {
+        __syncthreads();
+    } else {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+}
+
+// ---------------------------------------------------------- tensor memory --
+
+// Whole warp (of each CTA of the pair).  The column base goes to shared memory.
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t columns) {
+    if constexpr (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         atom::smem_u32(dst)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         atom::smem_u32(dst)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns)
-                 : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base),
+                     "r"(columns)
+                     : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base),
+                     "r"(columns)
+                     : "memory");
 }
 
 __device__ __forceinline__ void fence_before_sync() {
@@ -105,29 +166,39 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t format, bool a_mn, bo
            (b_mn ? 1u << 16 : 0u) | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
-// D (+)= A B, one thread.
-template <bool BF16>
+#define PURLIN_MMA(CG, KIND)                                                        \
+    asm volatile(                                                                   \
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"                             \
+        "tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d), \
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)                       \
+        : "memory")
+
+// D (+)= A B, one thread.  CG 2: the pair's leader, for both CTAs; A's rows and
+// B's columns lie half in each CTA's shared memory, at the same addresses.
+template <bool BF16, int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                     bool accumulate) {
-    if constexpr (BF16)
+    if constexpr (BF16 && CG == 1) PURLIN_MMA("1", "f16");
+    if constexpr (BF16 && CG == 2) PURLIN_MMA("2", "f16");
+    if constexpr (!BF16 && CG == 1) PURLIN_MMA("1", "f8f6f4");
+    if constexpr (!BF16 && CG == 2) PURLIN_MMA("2", "f8f6f4");
+}
+#undef PURLIN_MMA
+
+// Arrive on `bar` (of each CTA of the pair) when the products issued so far by
+// this thread are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+            ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
             : "memory");
-}
-
-// Arrive on `bar` when the products issued so far by this thread are done.
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
 }
 
 }  // namespace tensor

@@ -277,7 +277,7 @@ purlin_status purlin_noalloc_check(purlin_stream stream);
  * the same inputs give the same bits.  Partial results go to a workspace the
  * context owns, grown by the first call that needs more: during graph capture
  * such a call returns UNSUPPORTED, so make it once before.  rows, hidden, n
- * and k are below 2^31; offsets within a matrix may exceed 32 bits.  An
+ * and k are at most 2^31 - 4096; offsets within a matrix may exceed 32 bits.  An
  * output may not overlap another buffer (ALIAS) except where stated. */
 
 /* Root-mean-square norm with the residual's addition, for each row:
