@@ -26,6 +26,7 @@ struct NormArgs {
     float eps = 0;
     int dtype = 0, out_dtype = 0;
     int sms = 0;
+    unsigned long long *err = nullptr;
     cudaStream_t stream = nullptr;
 };
 
@@ -36,17 +37,18 @@ struct NormBackwardArgs {
     const void *dtotal = nullptr;   // or null
     void *dx = nullptr;
     float *dweight = nullptr;
-    float *partial = nullptr;       // norm_backward_ctas() x hidden
+    float *partial = nullptr;       // norm_backward_workspace() bytes
     size_t lddy = 0, ldt = 0, lddt = 0, lddx = 0;
     size_t rows = 0, hidden = 0;
     float eps = 0;
     int dtype = 0;
-    int ctas = 0;
+    int sms = 0;
+    unsigned long long *err = nullptr;
     cudaStream_t stream = nullptr;
 };
 
 cudaError_t launch_norm(const NormArgs &a);
-int norm_backward_ctas(size_t rows, size_t hidden, int dtype, int sms);
+size_t norm_backward_workspace(const NormBackwardArgs &a);
 cudaError_t launch_norm_backward(const NormBackwardArgs &a);
 
 // ------------------------------------------------------ grouped products --

@@ -190,6 +190,7 @@ purlin_status purlin_rms_norm(purlin_ctx *ctx, const void *x, size_t ldx, const 
     a.dtype = dtype;
     a.out_dtype = out_dtype;
     a.sms = ctx->sms;
+    a.err = ctx->err;
     a.stream = ctx->stream;
     return launch_norm(a) == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA;
 }
@@ -247,11 +248,12 @@ purlin_status purlin_rms_norm_backward(purlin_ctx *ctx, const void *dy, size_t l
     a.hidden = hidden;
     a.eps = eps;
     a.dtype = dtype;
-    a.ctas = norm_backward_ctas(rows, hidden, dtype, ctx->sms);
+    a.sms = ctx->sms;
+    a.err = ctx->err;
     a.stream = ctx->stream;
     void *work = nullptr;
     const purlin_status st =
-        workspace(ctx, (size_t)a.ctas * hidden * sizeof(float), &work);
+        workspace(ctx, norm_backward_workspace(a), &work);
     if (st != PURLIN_OK) return st;
     a.partial = static_cast<float *>(work);
     return launch_norm_backward(a) == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA;

@@ -67,6 +67,7 @@ enum ErrSite : uint64_t {
     kSiteChannelArgs = 8,  // a packet-channel unit past the channel's capacity
     kSiteGroups = 9,       // a group of a grouped product that lies outside its rows
     kSiteGroupedWait = 10, // a tile of a grouped product that never arrived
+    kSiteRowWait = 11,     // a row of a norm that never arrived
 };
 
 struct Ctl {

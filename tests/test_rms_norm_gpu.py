@@ -364,3 +364,71 @@ def test_side_stream_and_graph(P):
             assert bool(((dw.double() - dw64).abs() <= 200 * U * size).all())
     finally:
         c.close()
+
+
+# rows enough for persistent blocks that bring rows through shared memory: one to
+# five blocks an SM, two to four stages, every window edge, both operand counts
+MANY = [(2600, 1032), (2500, 1027), (1900, 4096), (1700, 4099), (1000, 7168), (700, 8192),
+        (640, 16384), (640, 16379), (3000, 2049)]
+
+
+@pytest.mark.parametrize("dtype,out", [(0, 0), (1, 1), (0, 2), (1, 2)],
+                         ids=["f32", "bf16", "f32-e4m3", "bf16-e4m3"])
+@pytest.mark.parametrize("rows,hidden", MANY)
+@pytest.mark.parametrize("residual", [False, True])
+def test_forward_many_rows(P, ctx, dtype, out, rows, hidden, residual):
+    dt = T[dtype]
+    x = randn(rows, hidden, seed=80, dtype=dt)
+    res = randn(rows, hidden, seed=81, dtype=dt) if residual else None
+    w = randn(hidden, seed=82, dtype=dt)
+    y = torch.empty(rows, hidden, device="cuda", dtype=torch.float8_e4m3fn if out == 2 else dt)
+    tot = torch.empty_like(x)
+    scales = torch.empty(rows, device="cuda") if out == 2 else None
+    P.purlin_rms_norm(ctx, x, w, y, rows, hidden, EPS, dtype, out, residual=res, total=tot,
+                      scales=scales)
+    P.purlin_check(ctx)
+    t64, v64 = forward64(x, res, w)
+    assert_close(tot, t64, 2 * U)
+    if out != 2:
+        assert_close(y, v64, slack(hidden) * 1.01)
+        return
+    want = (v64.abs().amax(1) / 448).clamp_min(2.0 ** -126)
+    assert_close(scales, want, (slack(hidden) + 4 * U) * 1.01)
+    q64 = v64 / want[:, None]
+    bound = torch.maximum(q64.abs() * 2.0 ** -4, torch.full_like(q64, 2.0 ** -10))
+    bound = bound + q64.abs() * 2 * (slack(hidden) + 4 * U)
+    assert bool(((y.float().double() - q64).abs() <= bound * 1.01).all())
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,hidden", MANY)
+@pytest.mark.parametrize("stream_grad", [False, True], ids=["plain", "dtotal"])
+def test_backward_many_rows(P, ctx, dtype, rows, hidden, stream_grad):
+    test_backward(P, ctx, dtype, rows, hidden, stream_grad)
+
+
+def test_many_rows_in_place_and_offset(P, ctx):
+    """Views that start in the middle of a window, rows enough to be staged, and
+    results over the inputs: a block fetches rows ahead of the ones it writes."""
+    rows, hidden, off = 1500, 4099, 5
+    bufs = [torch.empty(rows * hidden + 16, device="cuda", dtype=torch.bfloat16)
+            for _ in range(3)]
+    x, res, dy = (b[off:off + rows * hidden].view(rows, hidden) for b in bufs)
+    for k, t in enumerate((x, res, dy)):
+        t.copy_(randn(rows, hidden, seed=90 + k, dtype=torch.bfloat16))
+    w = randn(hidden + 3, seed=93, dtype=torch.bfloat16)[3:]
+    t64, v64 = forward64(x, res, w)
+    P.purlin_rms_norm(ctx, x, w, x, rows, hidden, EPS, 1, residual=res, total=res)
+    P.purlin_check(ctx)
+    assert_close(x, v64, slack(hidden) * 1.01)
+    assert_close(res, t64, 2 * U)
+    dx64, dw64 = backward64(res, dy, w, x)
+    g, td = (dy.double() * w.double()).abs(), res.double().abs()
+    r = 1 / torch.sqrt(res.double().square().mean(1, keepdim=True) + EPS)
+    scale = r * (g + td * r * r * (g * td).mean(1, keepdim=True)) + x.double().abs()
+    size = (dy.double() * res.double() * r).abs().sum(0)
+    dw = torch.empty(hidden, device="cuda")
+    P.purlin_rms_norm_backward(ctx, dy, res, w, dy, dw, rows, hidden, EPS, 1, dtotal=x)
+    P.purlin_check(ctx)
+    assert_rounds(dy, dx64, 4 * slack(hidden) * scale + 1e-37)
+    assert bool(((dw.double() - dw64).abs() <= (rows * U + 2 * slack(hidden)) * size + 1e-37).all())
