@@ -46,14 +46,17 @@ constexpr int kThreads = 64 + 32 * kWriters;
 constexpr int kSlotFloats = kTileI * kTileJ;      // one partial accumulator
 constexpr int kWidths = 8;                        // row-tile widths to choose from: 32, 64, ... 256
 
-// A CTA's share of B is half a pair's tile: two more stages fit.
-template <int CG>
-struct Ring {
-    static constexpr int kBBytes = kTileJ / CG * kRowBytes;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = CG == 1 ? 4 : 6;
-    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
-};
+constexpr uint32_t kRingBytes = 192 * 1024, kSmem = kRingBytes + 1024;
+constexpr int kMaxStages = 9;
+
+// Bytes of a stage: A's and the CTA's share of B.  A narrow tile leaves room for
+// more stages, which a stream of weights needs.
+template <bool B_MN, int CG>
+__device__ __forceinline__ uint32_t stage_bytes(int width) {
+    const int mine = width / CG;
+    return kABytes + (B_MN ? (mine + 63) / 64 * kBoxBytes
+                           : (mine + kBoxJ - 1) / kBoxJ * kBoxJ * kRowBytes);
+}
 
 struct TcParams {
     CUtensorMap a, b;
@@ -219,7 +222,9 @@ __device__ bool make_plan(Plan &t, const TcParams &p, int i_tiles, int ctas) {
 struct TcShared {
     Plan plan;
     snac::Ctl ctl;
-    uint64_t full[6], empty[6];   // stage loaded (for the leader, in both CTAs); consumed
+    uint64_t full[kMaxStages];    // stage loaded; the leader's count both CTAs' loads
+    uint64_t empty[kMaxStages];   // stage consumed
+    uint64_t cut[kMaxStages];     // leader: the other CTA has cut its part of the stage
     uint64_t done[2], free[2];    // accumulator complete; accumulator read
     uint64_t drain;
     uint32_t tmem;
@@ -335,7 +340,6 @@ __device__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile snac::Ctl 
 template <int MODE, bool BF16, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_tc_kernel(const __grid_constant__ TcParams p) {
-    using R = Ring<CG>;
     constexpr int BK = BF16 ? 64 : 128;        // K elements a stage
     constexpr int KSTEP = BF16 ? 16 : 32;      // K elements an instruction
     constexpr bool A_MN = MODE != kGroupedNK, B_MN = MODE == kGroupedGrad;
@@ -349,9 +353,10 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
     if (warp == 0 && lane == 0) {
         tensor::prefetch_map(&p.a);
         tensor::prefetch_map(&p.b);
-        for (int i = 0; i < R::kStages; ++i) {
-            atom::mbar_init(&s.full[i], CG == 2 && rank == 0 ? 2 : 1);
+        for (int i = 0; i < kMaxStages; ++i) {
+            atom::mbar_init(&s.full[i], 1);
             atom::mbar_init(&s.empty[i], 1);
+            atom::mbar_init(&s.cut[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             atom::mbar_init(&s.done[i], 1);
@@ -362,6 +367,10 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
         s.ctl.abort = 0;
     }
     const int i_tiles = (p.ni + kTileI * CG - 1) / (kTileI * CG);
+    // Everything before this overlaps the end of the kernel before; nothing of its
+    // memory is touched until it is done.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!make_plan<MODE, BK, CG>(s.plan, p, i_tiles, groups)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             snac::record_error(p.err, PURLIN_ERR_INVALID_ARG, snac::kSiteGroups, 0);
@@ -382,9 +391,22 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
     };
-    uint32_t filled = 0;   // stages that this thread has filled
-    Walk<MODE, BK, CG> walk(p, plan, i_tiles, group, groups);
     Unit q;
+    const uint32_t stage_size = stage_bytes<B_MN, CG>(plan.width);
+    const uint32_t stages = min((uint32_t)kMaxStages, kRingBytes / stage_size);
+    uint32_t filled = 0;           // stages that this thread has filled
+    uint32_t st = 0, parity = 0;   // the next stage, and its barriers' phase
+    auto advance = [&] {
+        if (++st == stages) {
+            st = 0;
+            parity ^= 1;
+        }
+    };
+    // whether a K block of the weight gradient ends inside an instruction's rows
+    auto cut_at = [&](int kb) {
+        return MODE == kGroupedGrad && min(BK, q.nk - kb * BK) % KSTEP != 0;
+    };
+    Walk<MODE, BK, CG> walk(p, plan, i_tiles, group, groups);
 
     if (warp < 2) {
         // One thread loads, one multiplies: nothing but them on a stage's path.
@@ -398,41 +420,46 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 const int boxes = B_MN ? (mine + 63) / 64 : (mine + kBoxJ - 1) / kBoxJ;
                 const uint32_t bytes = kABytes + boxes * (B_MN ? kBoxBytes : kBoxJ * kRowBytes);
                 const int i0 = q.i0 + rank * kTileI, j0 = q.j0 + rank * half;
-                for (int kb = q.kb0; kb < q.kb1; ++kb, ++filled) {
-                    const uint32_t st = filled % R::kStages;
-                    if (!wait(&s.empty[st], ((filled / R::kStages) & 1) ^ 1)) {
+                for (int kb = q.kb0; kb < q.kb1; ++kb, ++filled, advance()) {
+                    if (!wait(&s.empty[st], parity ^ 1)) {
                         run = false;
                         break;
                     }
-                    const uint32_t bar = atom::smem_u32(&s.full[st]);
-                    const uint32_t a = stage0 + st * R::kStageBytes, b = a + kABytes;
-                    atom::mbar_arrive_expect_tx(&s.full[st], bytes);
+                    // The leader's barrier counts both CTAs' bytes, except of a stage
+                    // that the other CTA still has to cut: that counts there first.
+                    uint32_t bar = atom::smem_u32(&s.full[st]);
+                    const bool apart = CG == 1 || cut_at(kb);
+                    if (rank == 0 || apart)
+                        atom::mbar_arrive_expect_tx(&s.full[st], apart ? bytes : 2 * bytes);
+                    else
+                        bar = tensor::in_cta(bar, 0);
+                    const uint32_t a = stage0 + st * stage_size, b = a + kABytes;
                     if constexpr (MODE == kGroupedNK) {
-                        tensor::load_box_3d(a, &p.a, kb * BK, i0, q.g, bar);
+                        tensor::load_box_3d<CG>(a, &p.a, kb * BK, i0, q.g, bar);
                     } else if constexpr (MODE == kGroupedKN) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            tensor::load_box_3d(a + h * kBoxBytes, &p.a, i0 + 64 * h, kb * BK, q.g,
-                                                bar);
+                            tensor::load_box_3d<CG>(a + h * kBoxBytes, &p.a, i0 + 64 * h, kb * BK,
+                                                    q.g, bar);
                     } else {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            tensor::load_box_2d(a + h * kBoxBytes, &p.a, i0 + 64 * h,
-                                                q.row0 + kb * BK, bar);
+                            tensor::load_box_2d<CG>(a + h * kBoxBytes, &p.a, i0 + 64 * h,
+                                                    q.row0 + kb * BK, bar);
                     }
                     for (int h = 0; h < boxes; ++h) {
                         if constexpr (B_MN)
-                            tensor::load_box_2d(b + h * kBoxBytes, &p.b, j0 + 64 * h,
-                                                q.row0 + kb * BK, bar);
+                            tensor::load_box_2d<CG>(b + h * kBoxBytes, &p.b, j0 + 64 * h,
+                                                    q.row0 + kb * BK, bar);
                         else
-                            tensor::load_box_2d(b + h * kBoxJ * kRowBytes, &p.b, kb * BK,
-                                                q.row0 + j0 + kBoxJ * h, bar);
+                            tensor::load_box_2d<CG>(b + h * kBoxJ * kRowBytes, &p.b, kb * BK,
+                                                    q.row0 + j0 + kBoxJ * h, bar);
                     }
                 }
             }
         } else {
-            // ---- multiply; the pair's other CTA passes on that its stages are loaded
-            uint32_t it = 0, acc = 0;
+            // ---- multiply; in the pair's other CTA, only cut stages
+            uint32_t acc = 0, cuts = 0;   // cuts: phase of each stage's cuts, one bit each
             bool run = true;
             while (run && walk.next(q)) {
                 if (q.kb0 == q.kb1) continue;   // a sum over nothing
@@ -446,16 +473,17 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 const int columns = columns_of<CG>(q.nj);
                 const uint32_t idesc =
                     tensor::instr_desc(BF16 ? 1 : 0, A_MN, B_MN, kTileI * CG, columns);
-                for (int kb = q.kb0; kb < q.kb1; ++kb, ++it) {
-                    const uint32_t st = it % R::kStages;
-                    if (!wait(&s.full[st], (it / R::kStages) & 1)) {
+                for (int kb = q.kb0; kb < q.kb1; ++kb, advance()) {
+                    const bool cut = cut_at(kb);
+                    if (rank != 0 && !cut) continue;
+                    const uint32_t phase = rank == 0 ? parity : cuts >> st & 1;
+                    if (!wait(&s.full[st], phase)) {
                         run = false;
                         break;
                     }
-                    const uint32_t a = stage0 + st * R::kStageBytes, b = a + kABytes;
+                    const uint32_t a = stage0 + st * stage_size, b = a + kABytes;
                     const int left = min(BK, q.nk - kb * BK);
                     const int steps = (left + KSTEP - 1) / KSTEP;
-                    const bool cut = MODE == kGroupedGrad && left < steps * KSTEP;
                     if (cut) {
                         // rows past the group's end inside the last instruction's 16
                         const int boxes = 2 + (columns / CG + 63) / 64;
@@ -466,10 +494,17 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                                              "r"(0)
                                              : "memory");
                         tensor::fence_async_shared();
-                    }
-                    if (rank != 0) {
-                        tensor::arrive_cluster(tensor::in_cta(atom::smem_u32(&s.full[st]), 0), cut);
-                        continue;
+                        const uint32_t cut_phase = cuts >> st & 1;
+                        cuts ^= 1u << st;
+                        if (rank != 0) {
+                            tensor::arrive_cluster(
+                                tensor::in_cta(atom::smem_u32(&s.cut[st]), 0), true);
+                            continue;
+                        }
+                        if (CG == 2 && !wait(&s.cut[st], cut_phase)) {
+                            run = false;
+                            break;
+                        }
                     }
                     tensor::fence_after_sync();
                     const uint64_t da = tensor::operand_desc(a, kBoxBytes);
@@ -646,9 +681,10 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
     tensor::fence_after_sync();
     if (s.ctl.abort) {
         // a wait expired: let the copies and products in flight end before the exit
-        if (warp == 0)
-            for (uint32_t o = filled > R::kStages ? filled - R::kStages : 0; o < filled; ++o)
-                bounded_wait(&s.full[o % R::kStages], (o / R::kStages) & 1, &s.ctl, p.err, false);
+        // (a pair's copies count at the leader, whose own wait expires with them)
+        if (warp == 0 && rank == 0)
+            for (uint32_t o = filled > stages ? filled - stages : 0; o < filled; ++o)
+                bounded_wait(&s.full[o % stages], (o / stages) & 1, &s.ctl, p.err, false);
         if (warp == 1 && rank == 0) {
             if (tensor::elect()) tensor::commit<CG>(atom::smem_u32(&s.drain));
             bounded_wait(&s.drain, 0, &s.ctl, p.err, false);
@@ -698,20 +734,21 @@ bool make_map(CUtensorMap *m, const void *p, int dtype, int rank, size_t d0, siz
 
 template <int MODE, bool BF16, int CG>
 cudaError_t launch_tc(const GroupedArgs &a, const TcParams &p) {
-    constexpr uint32_t smem = Ring<CG>::kSmem;
     static const cudaError_t ready = cudaFuncSetAttribute(
-        grouped_tc_kernel<MODE, BF16, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        grouped_tc_kernel<MODE, BF16, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(a.sms / CG * CG));
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = smem;
+    c.dynamicSmemBytes = kSmem;
     c.stream = a.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {CG, 1, 1};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {CG, 1, 1};
     c.attrs = at;
-    c.numAttrs = CG == 1 ? 0 : 1;
+    c.numAttrs = CG;
     return cudaLaunchKernelEx(&c, grouped_tc_kernel<MODE, BF16, CG>, p);
 }
 

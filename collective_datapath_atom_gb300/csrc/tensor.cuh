@@ -31,24 +31,29 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
-// One box of a tensor into shared memory, completion counted on `bar`.
+// One box of a tensor into shared memory, completion counted on `bar`.  CG 2:
+// `bar` may be the pair's other CTA's (an address of in_cta).
+#define PURLIN_LOAD_BOX(DIM, GROUP, COORDS, ...)                                   \
+    asm volatile("cp.async.bulk.tensor." DIM                                       \
+                 ".shared::cluster.global.tile.mbarrier::complete_tx::bytes" GROUP \
+                 " [%0], [%1, " COORDS "], [%2];" ::"r"(smem),                     \
+                 "l"(m), "r"(bar), __VA_ARGS__                                     \
+                 : "memory")
+
+template <int CG>
 __device__ __forceinline__ void load_box_2d(uint32_t smem, const CUtensorMap *m, int c0, int c1,
                                             uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem),
-        "l"(m), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
+    if constexpr (CG == 1) PURLIN_LOAD_BOX("2d", "", "{%3, %4}", "r"(c0), "r"(c1));
+    else PURLIN_LOAD_BOX("2d", ".cta_group::2", "{%3, %4}", "r"(c0), "r"(c1));
 }
 
+template <int CG>
 __device__ __forceinline__ void load_box_3d(uint32_t smem, const CUtensorMap *m, int c0, int c1,
                                             int c2, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem),
-        "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
+    if constexpr (CG == 1) PURLIN_LOAD_BOX("3d", "", "{%3, %4, %5}", "r"(c0), "r"(c1), "r"(c2));
+    else PURLIN_LOAD_BOX("3d", ".cta_group::2", "{%3, %4, %5}", "r"(c0), "r"(c1), "r"(c2));
 }
+#undef PURLIN_LOAD_BOX
 
 // Writes of this thread to shared memory become visible to the async proxy.
 __device__ __forceinline__ void fence_async_shared() {
