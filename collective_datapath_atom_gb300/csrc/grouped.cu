@@ -14,11 +14,10 @@
 // accumulators in tensor memory, and eight warps write the other accumulator out
 // meanwhile.
 //
-// Tiles go round the CTAs in whole waves; what is left over, or everything when
-// there are fewer tiles than CTAs (decode), is cut into equal runs of K blocks
-// instead, one a CTA.  A run's partial tiles go to a workspace in binary32, and
-// the last of a tile's CTAs to arrive adds them in K order, so the result does
-// not depend on which came last.
+// Tiles go round the CTAs; fewer tiles than CTAs (decode) are cut into equal runs
+// of K blocks instead, one a CTA.  A run's partial tiles go to a workspace in
+// binary32, and the last of a tile's CTAs to arrive adds them in K order, so the
+// result does not depend on which came last.
 //
 // kGroupedGrad sums over a group's rows: both operands then lie along M or N in
 // memory (MN-major), and the last block of rows is cut at the group's end by
@@ -42,7 +41,8 @@ constexpr int kABytes = kTileI * kRowBytes;       // 16 KiB a stage
 constexpr int kBoxJ = 32;                         // rows of a K-major box of B
 constexpr int kBoxBytes = 64 * kRowBytes;         // MN-major box: 64 elements by 64 k
 constexpr int kWriters = 8;                       // warps that write accumulators out
-constexpr int kThreads = 64 + 32 * kWriters;
+constexpr int kCutter = 2 + kWriters;             // the warp that cuts stages (kGroupedGrad)
+constexpr int threads_of(int mode) { return 32 * (kCutter + (mode == kGroupedGrad ? 1 : 0)); }
 constexpr int kSlotFloats = kTileI * kTileJ;      // one partial accumulator
 constexpr int kWidths = 8;                        // row-tile widths to choose from: 32, 64, ... 256
 
@@ -75,14 +75,13 @@ struct TcParams {
 // The launch's tiles, found from the groups by every CTA.
 struct Plan {
     int tiles[kMaxGroups + 1];           // tiles before group g
-    long long blocks[kMaxGroups + 1];    // K blocks before group g, at least one a tile
+    long long cost[kMaxGroups + 1];      // cost of those tiles (block_cost)
     int begin[kMaxGroups];
     int count[kMaxGroups];
-    int down[kWidths];                   // row tiles of each width
     int width;                           // of a row tile
-    int whole;                           // tiles that go round in whole waves
-    int runs;                            // CTAs that share the others
-    long long first, left;               // K blocks before the others, and of them
+    int whole;                           // tiles that go round whole: all or none
+    int runs;                            // CTAs that share all of them instead
+    long long left;                      // cost of those
     int bad;
 };
 
@@ -99,132 +98,168 @@ __device__ __forceinline__ int group_of(const T *before, int groups, T at) {
     return lo;
 }
 
-// K blocks of one of group g's tiles; an empty sum counts as one.
-template <int MODE, int BK>
-__device__ __forceinline__ int tile_blocks(const TcParams &p, int count) {
-    return max(1, ((MODE == kGroupedGrad ? count : p.k) + BK - 1) / BK);
-}
+// Cost of a K block of a tile with nj columns: its loads, in KiB (A's 16 and an
+// eighth a column).
+constexpr int kMostCost = 16 + kTileJ / 8;
+__device__ __forceinline__ int block_cost(int nj) { return 16 + (nj + 7) / 8; }
 
-// Cost of a K block at a row-tile width, in clocks of an SM: the products, or
-// the fill of shared memory from L2 (measured: 47 bytes a clock).
+// The same in clocks of an SM: the products, or the fill of shared memory (about
+// 65 bytes a clock).
 template <int CG>
 __device__ __forceinline__ float block_clocks(int width) {
-    return fmaxf(2.f * width, (kABytes + (float)(width * kRowBytes / CG)) / 47.f);
+    return fmaxf(2.f * width, (kABytes + (float)(width * kRowBytes / CG)) / 65.f);
 }
 
 // A run's join costs about this many K blocks of time.
 constexpr int kJoinBlocks = 12;
 
-// Read and check the groups and lay out the tiles.  Every thread of the block
-// calls it; false if a group lies outside the rows or the groups hold more
-// rows than there are (so some overlap).
+// One group's tiles: `full` row tiles of the plan's width, then maybe a narrower
+// one, each of them i_tiles tiles.
+template <int MODE, int BK>
+struct GroupTiles {
+    int i_tiles, width, rest, blocks;
+    int full;                          // tiles of the whole width
+    long long full_cost, rest_cost;    // of one tile
+    __device__ GroupTiles(const TcParams &p, int count, int width, int i_tiles)
+        : i_tiles(i_tiles), width(width) {
+        const int nj = MODE == kGroupedGrad ? p.n : count;
+        blocks = max(1, ((MODE == kGroupedGrad ? count : p.k) + BK - 1) / BK);   // empty sums too
+        const int down = nj / width;
+        rest = nj - down * width;
+        full = down * i_tiles;
+        full_cost = (long long)blocks * block_cost(width);
+        rest_cost = (long long)blocks * block_cost(rest);
+    }
+    __device__ int tiles() const { return full + (rest > 0 ? i_tiles : 0); }
+    __device__ long long cost() const { return before(tiles()); }
+    __device__ long long before(int local) const {
+        return min(local, full) * full_cost + max(0, local - full) * rest_cost;
+    }
+    __device__ int tile_at(long long cost) const {
+        return cost < full * full_cost ? (int)(cost / full_cost)
+                                       : full + (int)((cost - full * full_cost) / rest_cost);
+    }
+    __device__ int unit(int local) const { return block_cost(local < full ? width : rest); }
+};
+
+// Whether group (b, c) lies in the rows.
+__device__ __forceinline__ bool group_bad(long long b, long long c, long long rows) {
+    return c < 0 || b < 0 || c > rows || b > rows - c;   // c > rows first: b + c does not overflow
+}
+
+// Warp 0: check the groups and lay out the tiles.  More than 32 groups are in the
+// plan already (`bad`: one of them lies outside the rows).  Groups that hold more
+// rows than there are overlap, and are refused too; a plan of bad groups has no
+// tiles.  This stands before the first load of every CTA, so it is one warp's
+// work with one block barrier behind it, and sums by redux (3100 clocks by block
+// and shared atomics, 5.3 us of a whole small product).
 template <int MODE, int BK, int CG>
-__device__ bool make_plan(Plan &t, const TcParams &p, int i_tiles, int ctas) {
-    if (threadIdx.x < kWidths) t.down[threadIdx.x] = 0;
-    if (threadIdx.x == 0) t.bad = 0;
-    __syncthreads();
-    for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
-        const long long b = p.begin[g], c = p.count[g];
-        // c > rows first: b + c does not overflow
-        const bool bad = c < 0 || b < 0 || c > p.rows || b > p.rows - c;
-        if (bad) t.bad = 1;
-        t.begin[g] = (int)b;
-        t.count[g] = (int)c;
-        if (!bad) {
-            const int j = MODE == kGroupedGrad ? p.n : (int)c;
-#pragma unroll
-            for (int w = 0; w < kWidths; ++w) atomicAdd(&t.down[w], (j + 32 * w + 31) / (32 * w + 32));
-        }
+__device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool bad) {
+    const int lane = threadIdx.x;
+    if (p.groups <= 32 && lane < p.groups) {
+        const long long b = p.begin[lane], c = p.count[lane];
+        bad = group_bad(b, c, p.rows);
+        t.begin[lane] = (int)b;
+        t.count[lane] = (int)c;
     }
-    __syncthreads();
-    if (t.bad) return false;
-    if (threadIdx.x < 32) {
-        // the width that costs least, the wider of two that cost the same
-        const int lane = threadIdx.x;
-        float cost = 3.4e38f;
-        if (lane < kWidths) {
-            const int w = 32 * lane + 32;
-            const float tiles = (float)t.down[lane] * i_tiles;
-            const float blocks = MODE == kGroupedGrad
-                                     ? fmaxf(1.f, (float)p.rows / (BK * (float)p.groups))
-                                     : (float)((p.k + BK - 1) / BK);
-            const float even = tiles / ctas, waves = ceilf(even);
-            cost = fminf(waves * blocks, even * blocks + kJoinBlocks) * block_clocks<CG>(w) + 12.f * w;
-        }
-        int width = 32 * lane + 32;
+    bad = __any_sync(0xffffffffu, bad);
+    long long held = 0;
+    int down[kWidths] = {};   // row tiles at each width
+    if (!bad) {
+        unsigned low = 0, high = 0;
+        for (int g = lane; g < p.groups; g += 32) {
+            const int c = t.count[g];
+            low += (unsigned)c & 0xFFFFu;
+            high += (unsigned)c >> 16;
+            if constexpr (MODE != kGroupedGrad) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float c = __shfl_xor_sync(0xffffffffu, cost, o);
-            const int w = __shfl_xor_sync(0xffffffffu, width, o);
-            if (c < cost || (c == cost && w > width)) {
-                cost = c;
-                width = w;
+                for (int w = 0; w < kWidths; ++w) down[w] += (c + 32 * w + 31) / (32 * w + 32);
             }
         }
-        int tiles = 0;
-        long long blocks = 0, held = 0;
-        for (int g0 = 0; g0 < p.groups; g0 += 32) {
-            const int g = g0 + lane;
-            const int c = g < p.groups ? t.count[g] : 0;
-            int v = g < p.groups ? ((MODE == kGroupedGrad ? p.n : c) + width - 1) / width * i_tiles : 0;
-            long long k = (long long)v * tile_blocks<MODE, BK>(p, c);
-            held += c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                const long long q = __shfl_up_sync(0xffffffffu, k, o);
-                if (lane >= o) {
-                    v += u;
-                    k += q;
-                }
-            }
-            if (g < p.groups) {
-                t.tiles[g + 1] = tiles + v;
-                t.blocks[g + 1] = blocks + k;
-            }
-            tiles += __shfl_sync(0xffffffffu, v, 31);
-            blocks += __shfl_sync(0xffffffffu, k, 31);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) held += __shfl_xor_sync(0xffffffffu, held, o);
-        __syncwarp();
+        held = ((long long)__reduce_add_sync(0xffffffffu, high) << 16) +
+               __reduce_add_sync(0xffffffffu, low);
+        bad = held > p.rows;
+    }
+    if (bad) {
         if (lane == 0) {
-            t.tiles[0] = 0;
-            t.blocks[0] = 0;
-            t.width = width;
-            if (held > p.rows) t.bad = 1;
-            // Runs of K blocks for what does not fill whole waves, where the time
-            // that idle CTAs would waste is more than a join's.
-            const int waves = (tiles + ctas - 1) / ctas;
-            int whole = tiles;
-            if (!t.bad && tiles % ctas != 0) {
-                const long long wasted = (long long)waves * ctas - tiles;
-                if (wasted * (blocks / tiles) >= (long long)kJoinBlocks * ctas)
-                    whole = max(0, waves - 2) * ctas;
-            }
-            t.whole = whole;
-            long long first = blocks;
-            if (whole < tiles) {
-                const int g = group_of(t.tiles, p.groups, whole);
-                first = t.blocks[g] + (long long)(whole - t.tiles[g]) *
-                                          tile_blocks<MODE, BK>(p, t.count[g]);
-            }
-            t.first = first;
-            t.left = blocks - first;
-            // at least four blocks a run
-            t.runs = (int)max(1ll, min((long long)ctas, t.left / 4));
+            t.bad = 1;
+            t.width = 32;
+            t.whole = 0;
+            t.left = 0;
+            t.runs = 1;
         }
+        return;
     }
-    __syncthreads();
-    return !t.bad;
+    // the width that costs least, the wider of two that cost about the same
+    int mine = 0;
+#pragma unroll
+    for (int w = 0; w < kWidths; ++w) {
+        const int v = MODE == kGroupedGrad ? (p.n + 32 * w + 31) / (32 * w + 32) * p.groups
+                                           : __reduce_add_sync(0xffffffffu, down[w]);
+        if (lane == w) mine = v;
+    }
+    unsigned key = 0xFFFFFFFFu;
+    if (lane < kWidths) {
+        const int w = 32 * lane + 32;
+        const float tiles = (float)mine * i_tiles;
+        const float blocks = MODE == kGroupedGrad
+                                 ? fmaxf(1.f, (float)held / (BK * (float)p.groups))
+                                 : (float)((p.k + BK - 1) / BK);
+        const float even = tiles / ctas, waves = ceilf(even);
+        const float cost = (even >= 1.f ? waves * blocks : fminf(blocks, even * blocks + kJoinBlocks)) *
+                               block_clocks<CG>(w) + 12.f * w;
+        key = (__float_as_uint(cost) & ~7u) | (unsigned)(kWidths - 1 - lane);
+    }
+    const int width = 32 * (kWidths - (int)(__reduce_min_sync(0xffffffffu, key) & 7u));
+    int tiles = 0;
+    long long spent = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+        const int g = g0 + lane;
+        const GroupTiles<MODE, BK> of(p, g < p.groups ? t.count[g] : 0, width, i_tiles);
+        int v = g < p.groups ? of.tiles() : 0;
+        long long k = g < p.groups ? of.cost() : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            const long long q = __shfl_up_sync(0xffffffffu, k, o);
+            if (lane >= o) {
+                v += u;
+                k += q;
+            }
+        }
+        if (g < p.groups) {
+            t.tiles[g + 1] = tiles + v;
+            t.cost[g + 1] = spent + k;
+        }
+        tiles += __shfl_sync(0xffffffffu, v, 31);
+        spent += __shfl_sync(0xffffffffu, k, 31);
+    }
+    if (lane != 0) return;
+    t.bad = 0;
+    t.tiles[0] = 0;
+    t.cost[0] = 0;
+    t.width = width;
+    // Fewer tiles than CTAs: runs of K blocks, where the time that idle CTAs would
+    // waste is more than a join's.  (More tiles go round whole: CTAs in step share
+    // what they read of the weights, and with the last wave cut into runs
+    // 2048 x 7168 x 2048 took 99 us instead of 65.)
+    const long long idle = ctas - tiles;
+    const bool cut = tiles > 0 && idle > 0 &&
+                     idle * (spent / tiles) >= (long long)kJoinBlocks * ctas * block_cost(width);
+    t.whole = cut ? 0 : tiles;
+    t.left = cut ? spent : 0;
+    // at least four of the dearest blocks a run: a block begins in each
+    t.runs = (int)max(1ll, min((long long)ctas, t.left / (4 * kMostCost)));
 }
 
 struct TcShared {
     Plan plan;
     snac::Ctl ctl;
-    uint64_t full[kMaxStages];    // stage loaded; the leader's count both CTAs' loads
+    uint64_t full[kMaxStages];    // stage loaded; the leader's counts both CTAs' loads
     uint64_t empty[kMaxStages];   // stage consumed
-    uint64_t cut[kMaxStages];     // leader: the other CTA has cut its part of the stage
+    // kGroupedGrad, in place of full where a stage is to be cut at the group's end:
+    uint64_t whole[kMaxStages];   // loaded in this CTA
+    uint64_t cut[kMaxStages];     // cut in both (leader)
     uint64_t done[2], free[2];    // accumulator complete; accumulator read
     uint64_t drain;
     uint32_t tmem;
@@ -240,12 +275,14 @@ struct Unit {
     int kb0, kb1;        // kb0 == kb1: the sum over nothing
     int tile;
     int c0, c1;          // the tile's runs, first and last; equal where nobody shares it
+    long long begin;     // of a run's tile: where its cost begins among them
 };
 
+// The runs split the cost evenly; a block belongs to the run it begins in.
 __device__ __forceinline__ long long run_begin(const Plan &t, int c) { return t.left * c / t.runs; }
 
-__device__ __forceinline__ int run_of(const Plan &t, long long block) {
-    return (int)(((block + 1) * t.runs - 1) / t.left);
+__device__ __forceinline__ int run_of(const Plan &t, long long at) {
+    return (int)(((at + 1) * t.runs - 1) / t.left);
 }
 
 // Walks the units of one CTA (or pair) `c` of `ctas`.
@@ -255,7 +292,7 @@ struct Walk {
     const Plan &t;
     int i_tiles, c, ctas;
     int tile;             // next whole tile
-    long long at, end;    // the run's blocks still to do
+    long long at, end;    // the run's share of the cost still to do
     __device__ Walk(const TcParams &p, const Plan &t, int i_tiles, int c, int ctas)
         : p(p), t(t), i_tiles(i_tiles), c(c), ctas(ctas), tile(c) {
         at = end = 0;
@@ -275,30 +312,28 @@ struct Walk {
             q.c0 = q.c1 = c;
             return true;
         }
-        if (at >= end) return false;
-        const long long block = t.first + at;
-        q.g = group_of(t.blocks, p.groups, block);
-        const int each = tile_blocks<MODE, BK>(p, t.count[q.g]);
-        const int local = (int)((block - t.blocks[q.g]) / each);
-        q.tile = t.tiles[q.g] + local;
-        const long long begin = t.blocks[q.g] + (long long)local * each - t.first;
-        place(q);
-        q.kb0 = (int)(at - begin);
-        q.kb1 = (int)(min(end, begin + each) - begin);
-        at = begin + q.kb1;
-        q.c0 = run_of(t, begin);
-        q.c1 = run_of(t, begin + each - 1);
-        if (q.nk == 0) q.kb1 = q.kb0;
-        return true;
+        while (at < end) {
+            q.g = group_of(t.cost, p.groups, at);
+            const GroupTiles<MODE, BK> of(p, t.count[q.g], t.width, i_tiles);
+            const int local = of.tile_at(at - t.cost[q.g]), unit = of.unit(local);
+            q.tile = t.tiles[q.g] + local;
+            q.begin = t.cost[q.g] + of.before(local);
+            q.kb0 = (int)((at - q.begin + unit - 1) / unit);
+            q.kb1 = (int)min((long long)of.blocks, (end - q.begin + unit - 1) / unit);
+            at = q.begin + (long long)of.blocks * unit;
+            if (q.kb0 >= q.kb1) continue;   // the run begins inside the tile's last block
+            q.c0 = run_of(t, q.begin);
+            q.c1 = run_of(t, q.begin + (long long)(of.blocks - 1) * unit);
+            place(q);
+            if (q.nk == 0) q.kb1 = q.kb0;
+            return true;
+        }
+        return false;
     }
-    // Where run r's partial of the tile with K block `begin` lies: a run has at
+    // Where run r's partial of the tile that begins at `begin` lies: a run has at
     // most two, of the tile it begins in and of the one it ends in.
     __device__ int slot(int r, long long begin) const {
         return 2 * r + (run_begin(t, r) >= begin ? 0 : 1);
-    }
-    __device__ long long tile_begin(const Unit &q) const {
-        return t.blocks[q.g] - t.first +
-               (long long)(q.tile - t.tiles[q.g]) * tile_blocks<MODE, BK>(p, t.count[q.g]);
     }
     __device__ void place(Unit &q) const {
         const int local = q.tile - t.tiles[q.g];
@@ -338,7 +373,7 @@ __device__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile snac::Ctl 
 }
 
 template <int MODE, bool BF16, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(MODE), 1)
 grouped_tc_kernel(const __grid_constant__ TcParams p) {
     constexpr int BK = BF16 ? 64 : 128;        // K elements a stage
     constexpr int KSTEP = BF16 ? 16 : 32;      // K elements an instruction
@@ -356,7 +391,8 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
         for (int i = 0; i < kMaxStages; ++i) {
             atom::mbar_init(&s.full[i], 1);
             atom::mbar_init(&s.empty[i], 1);
-            atom::mbar_init(&s.cut[i], 1);
+            atom::mbar_init(&s.whole[i], 1);
+            atom::mbar_init(&s.cut[i], CG);
         }
         for (int i = 0; i < 2; ++i) {
             atom::mbar_init(&s.done[i], 1);
@@ -366,23 +402,29 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
         atom::mbar_init_fence();
         s.ctl.abort = 0;
     }
+    if (warp == 1) tensor::tmem_alloc<CG>(&s.tmem, 512);
     const int i_tiles = (p.ni + kTileI * CG - 1) / (kTileI * CG);
     // Everything before this overlaps the end of the kernel before; nothing of its
     // memory is touched until it is done.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!make_plan<MODE, BK, CG>(s.plan, p, i_tiles, groups)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            snac::record_error(p.err, PURLIN_ERR_INVALID_ARG, snac::kSiteGroups, 0);
-        return;
+    Plan &plan = s.plan;
+    bool bad = false;
+    if (p.groups > 32) {
+        for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
+            const long long b = p.begin[g], c = p.count[g];
+            bad |= group_bad(b, c, p.rows);
+            plan.begin[g] = (int)b;
+            plan.count[g] = (int)c;
+        }
+        bad = __syncthreads_or(bad);
     }
-    const Plan &plan = s.plan;
-    if (group >= plan.whole && (plan.left == 0 || group >= plan.runs)) return;   // nothing to do
-
-    if (warp == 1) tensor::tmem_alloc<CG>(&s.tmem, 512);
+    if (warp == 0) lay_out<MODE, BK, CG>(plan, p, i_tiles, groups, bad);
     tensor::fence_before_sync();
     tensor::sync_ctas<CG>();
     tensor::fence_after_sync();
+    if (plan.bad && blockIdx.x == 0 && threadIdx.x == 0)
+        snac::record_error(p.err, PURLIN_ERR_INVALID_ARG, snac::kSiteGroups, 0);
     const uint32_t tmem = s.tmem;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return bounded_wait(bar, parity, &s.ctl, p.err, true);
@@ -394,14 +436,16 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
     Unit q;
     const uint32_t stage_size = stage_bytes<B_MN, CG>(plan.width);
     const uint32_t stages = min((uint32_t)kMaxStages, kRingBytes / stage_size);
-    uint32_t filled = 0;           // stages that this thread has filled
-    uint32_t st = 0, parity = 0;   // the next stage, and its barriers' phase
+    uint32_t st = 0, parity = 0;   // the next stage, and its ring's turn
     auto advance = [&] {
         if (++st == stages) {
             st = 0;
             parity ^= 1;
         }
     };
+    // Phases of each stage's full (or whole and cut), one bit each: a stage's turn
+    // uses the one or the others.  For the loading thread, those it counted on.
+    uint32_t fulls = 0, cuts = 0, full_used = 0, cut_used = 0;
     // whether a K block of the weight gradient ends inside an instruction's rows
     auto cut_at = [&](int kb) {
         return MODE == kGroupedGrad && min(BK, q.nk - kb * BK) % KSTEP != 0;
@@ -420,19 +464,25 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 const int boxes = B_MN ? (mine + 63) / 64 : (mine + kBoxJ - 1) / kBoxJ;
                 const uint32_t bytes = kABytes + boxes * (B_MN ? kBoxBytes : kBoxJ * kRowBytes);
                 const int i0 = q.i0 + rank * kTileI, j0 = q.j0 + rank * half;
-                for (int kb = q.kb0; kb < q.kb1; ++kb, ++filled, advance()) {
+                for (int kb = q.kb0; kb < q.kb1; ++kb, advance()) {
                     if (!wait(&s.empty[st], parity ^ 1)) {
                         run = false;
                         break;
                     }
-                    // The leader's barrier counts both CTAs' bytes, except of a stage
-                    // that the other CTA still has to cut: that counts there first.
+                    // the leader's barrier counts both CTAs' bytes
                     uint32_t bar = atom::smem_u32(&s.full[st]);
-                    const bool apart = CG == 1 || cut_at(kb);
-                    if (rank == 0 || apart)
-                        atom::mbar_arrive_expect_tx(&s.full[st], apart ? bytes : 2 * bytes);
-                    else
+                    if (cut_at(kb)) {
+                        bar = atom::smem_u32(&s.whole[st]);
+                        atom::mbar_arrive_expect_tx(&s.whole[st], bytes);
+                        cuts ^= 1u << st;
+                        cut_used |= 1u << st;
+                    } else if (rank == 0) {
+                        atom::mbar_arrive_expect_tx(&s.full[st], CG * bytes);
+                        fulls ^= 1u << st;
+                        full_used |= 1u << st;
+                    } else {
                         bar = tensor::in_cta(bar, 0);
+                    }
                     const uint32_t a = stage0 + st * stage_size, b = a + kABytes;
                     if constexpr (MODE == kGroupedNK) {
                         tensor::load_box_3d<CG>(a, &p.a, kb * BK, i0, q.g, bar);
@@ -458,54 +508,34 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 }
             }
         } else {
-            // ---- multiply; in the pair's other CTA, only cut stages
-            uint32_t acc = 0, cuts = 0;   // cuts: phase of each stage's cuts, one bit each
-            bool run = true;
+            // ---- multiply: the pair's leader
+            uint32_t acc = 0;
+            bool run = rank == 0;
             while (run && walk.next(q)) {
                 if (q.kb0 == q.kb1) continue;   // a sum over nothing
                 const uint32_t buf = acc & 1;
-                if (rank == 0) {
-                    if (!wait(&s.free[buf], ((acc >> 1) & 1) ^ 1)) break;
-                    tensor::fence_after_sync();
-                }
+                if (!wait(&s.free[buf], ((acc >> 1) & 1) ^ 1)) break;
+                tensor::fence_after_sync();
                 ++acc;
                 const uint32_t d = tmem + buf * kTileJ;
-                const int columns = columns_of<CG>(q.nj);
-                const uint32_t idesc =
-                    tensor::instr_desc(BF16 ? 1 : 0, A_MN, B_MN, kTileI * CG, columns);
+                const uint32_t idesc = tensor::instr_desc(BF16 ? 1 : 0, A_MN, B_MN, kTileI * CG,
+                                                          columns_of<CG>(q.nj));
                 for (int kb = q.kb0; kb < q.kb1; ++kb, advance()) {
                     const bool cut = cut_at(kb);
-                    if (rank != 0 && !cut) continue;
-                    const uint32_t phase = rank == 0 ? parity : cuts >> st & 1;
-                    if (!wait(&s.full[st], phase)) {
+                    if (!wait(cut ? &s.cut[st] : &s.full[st], (cut ? cuts : fulls) >> st & 1)) {
                         run = false;
                         break;
+                    }
+                    if (cut) {
+                        cuts ^= 1u << st;
+                        // the other CTA's writes, which the products read there
+                        if constexpr (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    } else {
+                        fulls ^= 1u << st;
                     }
                     const uint32_t a = stage0 + st * stage_size, b = a + kABytes;
                     const int left = min(BK, q.nk - kb * BK);
                     const int steps = (left + KSTEP - 1) / KSTEP;
-                    if (cut) {
-                        // rows past the group's end inside the last instruction's 16
-                        const int boxes = 2 + (columns / CG + 63) / 64;
-                        for (int box = 0; box < boxes; ++box)
-                            for (int at = left * kRowBytes; at < steps * KSTEP * kRowBytes; at += 16)
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                 a + box * kBoxBytes + at),
-                                             "r"(0)
-                                             : "memory");
-                        tensor::fence_async_shared();
-                        const uint32_t cut_phase = cuts >> st & 1;
-                        cuts ^= 1u << st;
-                        if (rank != 0) {
-                            tensor::arrive_cluster(
-                                tensor::in_cta(atom::smem_u32(&s.cut[st]), 0), true);
-                            continue;
-                        }
-                        if (CG == 2 && !wait(&s.cut[st], cut_phase)) {
-                            run = false;
-                            break;
-                        }
-                    }
                     tensor::fence_after_sync();
                     const uint64_t da = tensor::operand_desc(a, kBoxBytes);
                     const uint64_t db = tensor::operand_desc(b, kBoxBytes);
@@ -519,6 +549,35 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                                                   kb > q.kb0 || k > 0);
                     tensor::commit<CG>(atom::smem_u32(&s.empty[st]));
                     if (kb + 1 == q.kb1) tensor::commit<CG>(atom::smem_u32(&s.done[buf]));
+                }
+            }
+        }
+    } else if (warp == kCutter) {
+        // ---- cut: clear the rows past a group's end inside the last instruction's 16
+        bool run = true;
+        while (run && walk.next(q)) {
+            const int boxes = 2 + (columns_of<CG>(q.nj) / CG + 63) / 64;
+            for (int kb = q.kb0; kb < q.kb1; ++kb, advance()) {
+                if (!cut_at(kb)) continue;
+                if (!wait_warp(&s.whole[st], cuts >> st & 1)) {
+                    run = false;
+                    break;
+                }
+                cuts ^= 1u << st;
+                const int left = q.nk - kb * BK, past = (left + KSTEP - 1) / KSTEP * KSTEP;
+                const int quads = (past - left) * (kRowBytes / 16);
+                const uint32_t from = stage0 + st * stage_size + left * kRowBytes;
+                for (int box = 0; box < boxes; ++box)
+                    for (int e = lane; e < quads; e += 32)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         from + box * kBoxBytes + e * 16),
+                                     "r"(0)
+                                     : "memory");
+                tensor::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1) atom::mbar_arrive(&s.cut[st]);
+                    else tensor::arrive_cluster(tensor::in_cta(atom::smem_u32(&s.cut[st]), 0), true);
                 }
             }
         }
@@ -608,10 +667,9 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 }
             } else {
                 // slot: [column / 4][lane of 128][4 columns]
-                const long long begin = walk.tile_begin(q);
                 auto slot_of = [&](int r) {
                     return reinterpret_cast<float4 *>(p.partial) +
-                           ((size_t)walk.slot(r, begin) * CG + rank) * (kSlotFloats / 4) +
+                           ((size_t)walk.slot(r, q.begin) * CG + rank) * (kSlotFloats / 4) +
                            quarter * 32 + lane;
                 };
                 float4 *mine = slot_of(group);
@@ -627,7 +685,7 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 __threadfence();
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
                 if (warp == 2 && lane == 0) {
-                    unsigned *n = p.arrived + (size_t)(q.tile - plan.whole) * CG + rank;
+                    unsigned *n = p.arrived + (size_t)q.tile * CG + rank;
                     s.last = atomicAdd(n, 1u) == (unsigned)(q.c1 - q.c0);
                     if (s.last) *n = 0;
                 }
@@ -635,31 +693,41 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                 if (s.last && !dead) {
                     __threadfence();
                     for (int c = c_first; c < q.nj; c += kColStep) {
-                        float sum[32];
-                        fetch(c, v);   // this CTA's own
+                        // eight loads in flight: four runs' partials of eight columns
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) sum[x] = 0.f;
-                        for (int r = q.c0; r <= q.c1; ++r) {
-                            if (r == group) {
+                        for (int x = 0; x < 8; x += 2) {
+                            float4 sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                            if (c + 4 * x < q.nj) {
+                                for (int r = q.c0; r <= q.c1; r += 4) {
+                                    float4 u[4][2];
 #pragma unroll
-                                for (int x = 0; x < 32; ++x) sum[x] += v[x];
-                                continue;
+                                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                        for (int y = 0; y < 2; ++y)
+                                            u[k][y] = r + k <= q.c1 && c + 4 * (x + y) < q.nj
+                                                          ? __ldcg(slot_of(r + k) +
+                                                                   (size_t)(c / 4 + x + y) * kTileI)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                        for (int y = 0; y < 2; ++y) {
+                                            sum[y].x += u[k][y].x;
+                                            sum[y].y += u[k][y].y;
+                                            sum[y].z += u[k][y].z;
+                                            sum[y].w += u[k][y].w;
+                                        }
+                                }
                             }
-                            const float4 *from = slot_of(r);
-                            float4 u[8];
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                u[x] = c + 4 * x < q.nj ? __ldcg(from + (size_t)(c / 4 + x) * kTileI)
-                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                sum[4 * x] += u[x].x;
-                                sum[4 * x + 1] += u[x].y;
-                                sum[4 * x + 2] += u[x].z;
-                                sum[4 * x + 3] += u[x].w;
+                            for (int y = 0; y < 2; ++y) {
+                                v[4 * (x + y)] = sum[y].x;
+                                v[4 * (x + y) + 1] = sum[y].y;
+                                v[4 * (x + y) + 2] = sum[y].z;
+                                v[4 * (x + y) + 3] = sum[y].w;
                             }
                         }
-                        put(c, sum);
+                        put(c, v);
                     }
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");   // s.last is free again
@@ -682,9 +750,13 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
     if (s.ctl.abort) {
         // a wait expired: let the copies and products in flight end before the exit
         // (a pair's copies count at the leader, whose own wait expires with them)
-        if (warp == 0 && rank == 0)
-            for (uint32_t o = filled > stages ? filled - stages : 0; o < filled; ++o)
-                bounded_wait(&s.full[o % stages], (o / stages) & 1, &s.ctl, p.err, false);
+        if (warp == 0)
+            for (uint32_t i = 0; i < stages; ++i) {
+                if (full_used >> i & 1)
+                    bounded_wait(&s.full[i], (fulls >> i & 1) ^ 1, &s.ctl, p.err, false);
+                if (cut_used >> i & 1)
+                    bounded_wait(&s.whole[i], (cuts >> i & 1) ^ 1, &s.ctl, p.err, false);
+            }
         if (warp == 1 && rank == 0) {
             if (tensor::elect()) tensor::commit<CG>(atom::smem_u32(&s.drain));
             bounded_wait(&s.drain, 0, &s.ctl, p.err, false);
@@ -739,7 +811,7 @@ cudaError_t launch_tc(const GroupedArgs &a, const TcParams &p) {
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(a.sms / CG * CG));
-    c.blockDim = dim3(kThreads);
+    c.blockDim = dim3(threads_of(MODE));
     c.dynamicSmemBytes = kSmem;
     c.stream = a.stream;
     cudaLaunchAttribute at[2];
