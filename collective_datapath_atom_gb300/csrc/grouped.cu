@@ -264,7 +264,8 @@ struct TcShared {
     uint64_t drain;
     uint32_t tmem;
     int last;
-    alignas(16) __nv_bfloat16 turn[kWriters][16][32];   // 16 rows of 32 channels a warp
+    alignas(16) __nv_bfloat16 turn[kWriters][16 * 32];   // 16 rows of 32 channels a warp
+    float row_scales[2][kTileJ];                         // of the tile at hand, and the next
 };
 
 // What a CTA (or pair) does next: K blocks [kb0, kb1) of a tile.
@@ -275,7 +276,7 @@ struct Unit {
     int kb0, kb1;        // kb0 == kb1: the sum over nothing
     int tile;
     int c0, c1;          // the tile's runs, first and last; equal where nobody shares it
-    long long begin;     // of a run's tile: where its cost begins among them
+    int head;            // the first run's slot for the tile; the others begin in it: 2 run
 };
 
 // The runs split the cost evenly; a block belongs to the run it begins in.
@@ -317,23 +318,19 @@ struct Walk {
             const GroupTiles<MODE, BK> of(p, t.count[q.g], t.width, i_tiles);
             const int local = of.tile_at(at - t.cost[q.g]), unit = of.unit(local);
             q.tile = t.tiles[q.g] + local;
-            q.begin = t.cost[q.g] + of.before(local);
-            q.kb0 = (int)((at - q.begin + unit - 1) / unit);
-            q.kb1 = (int)min((long long)of.blocks, (end - q.begin + unit - 1) / unit);
-            at = q.begin + (long long)of.blocks * unit;
+            const long long begin = t.cost[q.g] + of.before(local);
+            q.kb0 = (int)((at - begin + unit - 1) / unit);
+            q.kb1 = (int)min((long long)of.blocks, (end - begin + unit - 1) / unit);
+            at = begin + (long long)of.blocks * unit;
             if (q.kb0 >= q.kb1) continue;   // the run begins inside the tile's last block
-            q.c0 = run_of(t, q.begin);
-            q.c1 = run_of(t, q.begin + (long long)(of.blocks - 1) * unit);
+            q.c0 = run_of(t, begin);
+            q.c1 = run_of(t, begin + (long long)(of.blocks - 1) * unit);
+            q.head = 2 * q.c0 + (run_begin(t, q.c0) < begin ? 1 : 0);
             place(q);
             if (q.nk == 0) q.kb1 = q.kb0;
             return true;
         }
         return false;
-    }
-    // Where run r's partial of the tile that begins at `begin` lies: a run has at
-    // most two, of the tile it begins in and of the one it ends in.
-    __device__ int slot(int r, long long begin) const {
-        return 2 * r + (run_begin(t, r) >= begin ? 0 : 1);
     }
     __device__ void place(Unit &q) const {
         const int local = q.tile - t.tiles[q.g];
@@ -583,103 +580,140 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
         }
     } else {
         // ---- write out; warp w reads lanes 32 (w % 4) on of the accumulator, and
-        // every other 32 columns of them
-        const int quarter = warp & 3, c_first = 32 * ((warp - 2) >> 2);
-        constexpr int kColStep = 32 * kWriters / 4;
-        uint32_t acc = 0;
-        bool dead = false;   // a wait expired: walk on, for the barriers of shared tiles
+        // every other 16 columns of them
+        const int quarter = warp & 3;
+        constexpr int kColStep = 16 * kWriters / 4;
+        const int c_first = 16 * ((warp - 2) >> 2);
+        const uint32_t turn = atom::smem_u32(s.turn[warp - 2]);
+        // 16-byte pieces of a row of `turn` (32 channels) lie at a place that depends
+        // on the row: eight rows of one piece, and four pieces of a row, meet no bank twice
+        auto piece = [&](int r, int k) { return turn + r * 64 + ((k ^ (r >> 1)) & 3) * 16; };
+        uint32_t acc = 0, tile = 0;
+        bool dead = false;   // a wait expired: walk on, for the barriers of the writers
         while (walk.next(q)) {
-            const int i = q.i0 + rank * kTileI + quarter * 32 + lane;
-            const bool live = i < p.ni, shared = q.c0 != q.c1;
+            const int i0 = q.i0 + rank * kTileI + quarter * 32;   // the warp's first channel
+            const bool shared = q.c0 != q.c1;
             const bool empty = q.kb0 == q.kb1;
             const uint32_t buf = acc & 1;
+            const size_t row = MODE == kGroupedGrad ? (size_t)q.g * p.n + q.j0
+                                                    : (size_t)q.row0 + q.j0;
+            __nv_bfloat16 *out = p.out + row * p.ldy + i0;
+            // scales, fetched while the products go on
+            const float *xs = s.row_scales[tile++ & 1];
+            float ws[4];
+            if constexpr (!BF16) {
+                const int j = (int)threadIdx.x - 64;
+                if (j < q.nj) s.row_scales[(tile - 1) & 1][j] = p.x_scales[row + j];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int i = i0 + 8 * m + (lane >> 2);
+                    ws[m] = i < p.ni ? p.w_scales[(size_t)q.g * p.n + i] : 0.f;
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
+            }
             if (!empty && !dead) {
                 dead = !wait_warp(&s.done[buf], (acc >> 1) & 1);
                 ++acc;
                 tensor::fence_after_sync();
             }
-            const size_t row = MODE == kGroupedGrad ? (size_t)q.g * p.n + q.j0
-                                                    : (size_t)q.row0 + q.j0;
-            __nv_bfloat16 *out = p.out + row * p.ldy + i;
-            float ws = 1.f;
-            if constexpr (!BF16) ws = live ? p.w_scales[(size_t)q.g * p.n + i] : 0.f;
-            // 32 columns of the accumulator from column c on
-            auto fetch = [&](int c, float (&v)[32]) {
+            // 16 columns of the accumulator from column c on, as fragments: r[0..7] of
+            // the warp's lanes 0..15, r[8..15] of the others
+            auto fetch = [&](int c, uint32_t (&r)[16]) {
                 __syncwarp();
                 if (!empty) {
-                    uint32_t r[32];
-                    tensor::tmem_load32(tmem + buf * kTileJ + c + ((uint32_t)quarter << 21), r);
-                    tensor::tmem_wait_loads();
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]);
+                    const uint32_t at = tmem + buf * kTileJ + c + ((uint32_t)quarter << 21);
+                    tensor::tmem_load_fragments(at, r);
+                    tensor::tmem_load_fragments(at + (16u << 16), r + 8);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = 0.f;
+                    for (int x = 0; x < 16; ++x) r[x] = 0;
                 }
             };
-            // Rows of out are rows of the accumulator's columns: sixteen at a time
-            // turn in shared memory, so that a store is 16 bytes and not 2 (an
-            // epilogue of 2-byte stores took 10 us a tile, five times this one).
-            auto put = [&](int c, float (&v)[32]) {
-                const int width = min(32, q.nj - c);
-                if constexpr (!BF16) {
-                    const float xs = lane < width ? p.x_scales[row + c + lane] : 0.f;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = v[x] * __shfl_sync(0xffffffffu, xs, x) * ws;
-                }
-                if (!p.wide) {
-                    __nv_bfloat16 *to = out + (size_t)c * p.ldy;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        if (x < width && live) *to = __float2bfloat16_rn(v[x]);
-                        to += p.ldy;
-                    }
-                    return;
-                }
-                __nv_bfloat16(&turn)[16][32] = s.turn[warp - 2];
-                const int ch = (lane & 3) * 8, room = p.ni - (i - lane) - ch;
+            // Rows of out are columns of the accumulator: they turn in shared memory by
+            // stmatrix, and leave as 16-byte stores where out's rows allow it.
+            auto put = [&](int c, const uint32_t (&r)[16]) {
+                __syncwarp();   // the rows before have left
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (16 * h >= width) break;
-                    __syncwarp();
+                    float2 sx = {1.f, 1.f};
+                    if constexpr (!BF16)
+                        sx = *reinterpret_cast<const float2 *>(xs + c + 8 * h + 2 * (lane & 3));
+                    uint32_t m[4];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) turn[x][lane] = __float2bfloat16_rn(v[16 * h + x]);
-                    __syncwarp();
+                    for (int k = 0; k < 4; ++k) {   // channels 8 k on
+                        const int at = 8 * (k >> 1) + 4 * h + 2 * (k & 1);
+                        float a = __uint_as_float(r[at]), b = __uint_as_float(r[at + 1]);
+                        if constexpr (!BF16) {
+                            a = a * sx.x * ws[k];
+                            b = b * sx.y * ws[k];
+                        }
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+                        m[k] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    tensor::store_transposed(piece(8 * h + (lane & 7), lane >> 3), m[0], m[1], m[2],
+                                             m[3]);
+                }
+                __syncwarp();
+                if (p.wide) {
+                    const int k = lane & 3, room = p.ni - i0 - 8 * k;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const int r = 8 * t + (lane >> 2), j = c + 16 * h + r;
-                        if (j >= q.nj || room <= 0) continue;
-                        __nv_bfloat16 *to = out - lane + ch + (size_t)j * p.ldy;
+                        const int rr = 8 * t + (lane >> 2);
+                        if (c + rr >= q.nj || room <= 0) continue;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(piece(rr, k))
+                                     : "memory");
+                        __nv_bfloat16 *to = out + 8 * k + (size_t)(c + rr) * p.ldy;
                         if (room >= 8) {
-                            *reinterpret_cast<uint4 *>(to) =
-                                *reinterpret_cast<const uint4 *>(&turn[r][ch]);
+                            *reinterpret_cast<uint4 *>(to) = v;
                         } else {
-                            for (int e = 0; e < room; ++e) to[e] = turn[r][ch + e];
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 7; ++e)
+                                if (e < room)
+                                    reinterpret_cast<unsigned short *>(to)[e] =
+                                        (unsigned short)(w[e / 2] >> 16 * (e % 2));
                         }
                     }
+                } else {
+                    unsigned short *to =
+                        reinterpret_cast<unsigned short *>(out) + lane + (size_t)c * p.ldy;
+                    const int rows = i0 + lane < p.ni ? q.nj - c : 0;
+                    unsigned short v[16];
+#pragma unroll
+                    for (int rr = 0; rr < 16; ++rr)
+                        asm volatile("ld.shared.u16 %0, [%1];"
+                                     : "=h"(v[rr])
+                                     : "r"(piece(rr, lane >> 3) + (lane & 7) * 2)
+                                     : "memory");
+#pragma unroll
+                    for (int rr = 0; rr < 16; ++rr, to += p.ldy)
+                        if (rr < rows) *to = v[rr];
                 }
             };
-            float v[32];
-            if (!shared) {
+            // Where run r's partial of the tile lies (a run has two slots: for the tile it
+            // begins in, and for the one it ends in if that is another):
+            // [16 columns][quarter of the fragments][lane of 128] of float4.
+            auto slot_of = [&](int r, int c) {
+                return reinterpret_cast<float4 *>(p.partial) +
+                       ((size_t)(r == q.c0 ? q.head : 2 * r) * CG + rank) * (kSlotFloats / 4) +
+                       (size_t)(c / 16) * 4 * kTileI + quarter * 32 + lane;
+            };
+            uint32_t r[16], ahead[16];
+            if (shared) {
                 for (int c = c_first; c < q.nj && !dead; c += kColStep) {
-                    fetch(c, v);
-                    put(c, v);
-                }
-            } else {
-                // slot: [column / 4][lane of 128][4 columns]
-                auto slot_of = [&](int r) {
-                    return reinterpret_cast<float4 *>(p.partial) +
-                           ((size_t)walk.slot(r, q.begin) * CG + rank) * (kSlotFloats / 4) +
-                           quarter * 32 + lane;
-                };
-                float4 *mine = slot_of(group);
-                for (int c = c_first; c < q.nj && !dead; c += kColStep) {
-                    fetch(c, v);
+                    fetch(c, r);
+                    tensor::tmem_wait_loads(r);
+                    float4 *mine = slot_of(group, c);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        if (c + 4 * x < q.nj)
-                            __stcg(mine + (size_t)(c / 4 + x) * kTileI,
-                                   make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
+                    for (int x = 0; x < 4; ++x)
+                        if (x % 2 == 0 || c + 8 < q.nj)
+                            __stcg(mine + x * kTileI,
+                                   make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                                               __uint_as_float(r[4 * x + 2]),
+                                               __uint_as_float(r[4 * x + 3])));
                 }
                 // the last of the tile's CTAs adds the accumulators in K order
                 __threadfence();
@@ -690,47 +724,50 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                     if (s.last) *n = 0;
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
-                if (s.last && !dead) {
-                    __threadfence();
-                    for (int c = c_first; c < q.nj; c += kColStep) {
-                        // eight loads in flight: four runs' partials of eight columns
+                if (s.last) __threadfence();
+                for (int c = c_first; c < q.nj && !dead && s.last; c += kColStep) {
+                    float4 sum[4] = {};
+                    for (int k = q.c0; k <= q.c1; k += 3) {
+                        float4 u[3][4];   // three runs' loads in flight
 #pragma unroll
-                        for (int x = 0; x < 8; x += 2) {
-                            float4 sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                            if (c + 4 * x < q.nj) {
-                                for (int r = q.c0; r <= q.c1; r += 4) {
-                                    float4 u[4][2];
+                        for (int y = 0; y < 3; ++y)
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k)
+                            for (int x = 0; x < 4; ++x)
+                                u[y][x] = k + y <= q.c1 && (x % 2 == 0 || c + 8 < q.nj)
+                                              ? __ldcg(slot_of(k + y, c) + x * kTileI)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                                        for (int y = 0; y < 2; ++y)
-                                            u[k][y] = r + k <= q.c1 && c + 4 * (x + y) < q.nj
-                                                          ? __ldcg(slot_of(r + k) +
-                                                                   (size_t)(c / 4 + x + y) * kTileI)
-                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int y = 0; y < 3; ++y)
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                        for (int y = 0; y < 2; ++y) {
-                                            sum[y].x += u[k][y].x;
-                                            sum[y].y += u[k][y].y;
-                                            sum[y].z += u[k][y].z;
-                                            sum[y].w += u[k][y].w;
-                                        }
-                                }
+                            for (int x = 0; x < 4; ++x) {
+                                sum[x].x += u[y][x].x;
+                                sum[x].y += u[y][x].y;
+                                sum[x].z += u[y][x].z;
+                                sum[x].w += u[y][x].w;
                             }
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                v[4 * (x + y)] = sum[y].x;
-                                v[4 * (x + y) + 1] = sum[y].y;
-                                v[4 * (x + y) + 2] = sum[y].z;
-                                v[4 * (x + y) + 3] = sum[y].w;
-                            }
-                        }
-                        put(c, v);
                     }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        r[4 * x] = __float_as_uint(sum[x].x);
+                        r[4 * x + 1] = __float_as_uint(sum[x].y);
+                        r[4 * x + 2] = __float_as_uint(sum[x].z);
+                        r[4 * x + 3] = __float_as_uint(sum[x].w);
+                    }
+                    put(c, r);
                 }
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");   // s.last is free again
+                // s.last is free again
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
+            } else if (!dead) {
+                // the next 16 columns are on their way while these are written
+                fetch(c_first, ahead);
+#pragma unroll 1
+                for (int c = c_first; c < q.nj; c += kColStep) {
+                    tensor::tmem_wait_loads(ahead);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) r[x] = ahead[x];
+                    if (c + kColStep < q.nj) fetch(c + kColStep, ahead);
+                    put(c, r);
+                }
             }
             if (!empty && !dead) {
                 tensor::fence_before_sync();
