@@ -864,14 +864,14 @@ cudaError_t launch_tc(const GroupedArgs &a, const TcParams &p) {
 template <int MODE, bool BF16>
 cudaError_t launch_mode(const GroupedArgs &a, const TcParams &p) {
     // A pair halves what each CTA loads of B, and its tiles are twice as wide: it
-    // pays where K is long and the groups fill its tiles.  16384 x 7168 x 2048 over 8
-    // groups: 323 us against 349 alone; K = 576 (5784 rows, 3 groups): 22.0 against
-    // 18.5; 10066 rows over 14 groups, 384 channels, forward K and backward: 80 against
-    // 74.  Channels that fill a wider tile badly stay with single CTAs.
-    const size_t per_group = a.rows / (size_t)a.groups;
-    const size_t kext = MODE == kGroupedGrad ? per_group : a.k;
+    // pays once there is work for it.  Single CTAs against pairs, us: 1024 rows in one
+    // group, 2048 x 2048, 13.2 and 14.0; 2048 rows in 8 groups, 1024 x 2048, 16.4 and
+    // 16.4, 7168 x 2048 69.1 and 64.3; 16384 rows in 64 groups, 2048 x 2048, 146 and 121;
+    // 16384 rows in 8, 7168 x 2048, 322 and 285.  Channels that fill a wider tile badly
+    // stay with single CTAs (384: a third of it empty).
+    const double work = (double)a.rows * (double)a.n * (double)a.k;
     const size_t wide = ((size_t)p.ni + 255) / 256 * 2, narrow = ((size_t)p.ni + 127) / 128;
-    const bool pair = kext >= 1024 && per_group >= 512 && 8 * wide <= 9 * narrow && a.sms >= 2;
+    const bool pair = work >= 8e9 && 8 * wide <= 9 * narrow && a.sms >= 2;
     return pair ? launch_tc<MODE, BF16, 2>(a, p) : launch_tc<MODE, BF16, 1>(a, p);
 }
 
