@@ -10,16 +10,21 @@ ctypes binding, so this module only marshals arguments.
     h = initialize(8, stream=torch.cuda.current_stream())
     all_reduce(xs, outs, h)                  # every outs[r] = sum over s of xs[s]
     finalize(h)
+
+The layer operators that follow the collectives take one rank's tensors:
+``rms_norm``, ``grouped_matmul`` and their gradients.
 """
 from __future__ import annotations
 
 import enum
 from typing import Sequence
 
-from . import (PURLIN_BF16, PURLIN_F32, Context, _stream_handle, purlin_all_gather,
-               purlin_all_gather_v, purlin_all_reduce, purlin_all_to_all, purlin_all_to_all_v,
-               purlin_check, purlin_finalize, purlin_init, purlin_reduce_scatter,
-               purlin_reduce_scatter_v, purlin_set_stream)
+from . import (PURLIN_BF16, PURLIN_E4M3, PURLIN_F32, PURLIN_WEIGHTS_KN, PURLIN_WEIGHTS_NK, Context,
+               _stream_handle, purlin_all_gather, purlin_all_gather_v, purlin_all_reduce,
+               purlin_all_to_all, purlin_all_to_all_v, purlin_check, purlin_finalize,
+               purlin_grouped_matmul, purlin_grouped_matmul_weight_grad, purlin_init,
+               purlin_reduce_scatter, purlin_reduce_scatter_v, purlin_rms_norm,
+               purlin_rms_norm_backward, purlin_set_stream)
 
 
 class ReductionMode(enum.Enum):
@@ -169,3 +174,155 @@ def all_to_all_v(xs, outs, counts, handle, stream=None):
             raise ValueError(f"output {dd} is shorter than its column of counts")
     _on(handle, stream)
     purlin_all_to_all_v(handle, xs, outs, flat, d)
+
+
+# ------------------------------------------------------- layer operators ---
+
+def _rows(name, t, dtypes, cols=None):
+    """(rows, cols, row stride) of a CUDA matrix whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(name, t, n, dtype):
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must hold {n} contiguous values on the GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+
+
+def _same_rows(name, t, like):
+    if t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    return _rows(name, t, (like.dtype,))[2]
+
+
+def rms_norm(x, weight, handle, residual=None, out=None, total=None, scales=None, eps=1e-5,
+             quantize=False, stream=None):
+    """Norm of the rows of ``x`` (+ ``residual``) times ``weight``.  Returns
+    ``out``, or ``(out, scales)`` with ``quantize`` (e4m3 rows, a float32 scale
+    a row); ``total``, if given, receives ``x + residual``.  Outputs are
+    allocated unless passed in."""
+    import torch
+
+    rows, hidden, ldx = _rows("x", x, (torch.float32, torch.bfloat16))
+    d = PURLIN_F32 if x.dtype == torch.float32 else PURLIN_BF16
+    _vector("weight", weight, hidden, x.dtype)
+    ldr = _same_rows("residual", residual, x) if residual is not None else 0
+    ldt = _same_rows("total", total, x) if total is not None else 0
+    kind = torch.float8_e4m3fn if quantize else x.dtype
+    if out is None:
+        out = torch.empty(rows, hidden, device=x.device, dtype=kind)
+    if out.shape != x.shape:
+        raise ValueError("out has the shape of x")
+    ldy = _rows("out", out, (kind,))[2]
+    if quantize and scales is None:
+        scales = torch.empty(rows, device=x.device)
+    if scales is not None:
+        if not quantize:
+            raise ValueError("scales belong to a quantized output")
+        _vector("scales", scales, rows, torch.float32)
+    _on(handle, stream)
+    purlin_rms_norm(handle, x, weight, out, rows, hidden, eps, d, PURLIN_E4M3 if quantize else d,
+                    residual=residual, total=total, scales=scales, ldx=ldx, ldr=ldr, ldy=ldy,
+                    ldt=ldt)
+    return (out, scales) if quantize else out
+
+
+def rms_norm_backward(dy, total, weight, handle, dtotal=None, dx=None, dweight=None, eps=1e-5,
+                      stream=None):
+    """Gradients of :func:`rms_norm` at ``total`` (``x + residual``): returns
+    ``(dx, dweight)``, dx that of x and of the residual, dweight in float32.
+    ``dtotal``: the gradient that reaches ``total`` from elsewhere."""
+    import torch
+
+    rows, hidden, ldt = _rows("total", total, (torch.float32, torch.bfloat16))
+    d = PURLIN_F32 if total.dtype == torch.float32 else PURLIN_BF16
+    _vector("weight", weight, hidden, total.dtype)
+    lddy = _same_rows("dy", dy, total)
+    lddt = _same_rows("dtotal", dtotal, total) if dtotal is not None else 0
+    dx = torch.empty(rows, hidden, device=dy.device, dtype=dy.dtype) if dx is None else dx
+    lddx = _same_rows("dx", dx, total)
+    dweight = torch.empty(hidden, device=dy.device) if dweight is None else dweight
+    _vector("dweight", dweight, hidden, torch.float32)
+    _on(handle, stream)
+    purlin_rms_norm_backward(handle, dy, total, weight, dx, dweight, rows, hidden, eps, d,
+                             dtotal=dtotal, lddy=lddy, ldt=ldt, lddt=lddt, lddx=lddx)
+    return dx, dweight
+
+
+def _stack(name, t, dtypes):
+    """(groups, rows, cols, row stride) of matrices that lie one after another."""
+    if not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or \
+            (t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1)):
+        raise ValueError(f"{name} must be CUDA matrices with contiguous rows, one after another")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return (*t.shape, t.stride(1))
+
+
+def _groups(begin, count, groups):
+    import torch
+
+    _vector("begin", begin, groups, torch.int64)
+    _vector("count", count, groups, torch.int64)
+
+
+def grouped_matmul(x, w, begin, count, handle, out=None, x_scales=None, w_scales=None,
+                   transposed=False, stream=None):
+    """Rows ``begin[g]`` to ``begin[g] + count[g]`` of ``x`` times the transpose
+    of ``w[g]`` (``w``: groups x n x k), or times ``w[g]`` itself (groups x k x
+    n) with ``transposed``, which with the output's gradient in place of ``x``
+    is the gradient of x.  bf16, or e4m3 with a scale a row of x and a channel
+    of w.  Rows of ``out`` in no group are left as they are (zero where it is
+    allocated here)."""
+    import torch
+
+    kinds = (torch.bfloat16, torch.float8_e4m3fn)
+    groups, wr, wc, ldw = _stack("w", w, kinds)
+    n, k = (wc, wr) if transposed else (wr, wc)
+    rows, _, ldx = _rows("x", x, (w.dtype,), k)
+    _groups(begin, count, groups)
+    if out is None:
+        out = torch.zeros(rows, n, device=x.device, dtype=torch.bfloat16)
+    out_rows, _, ldy = _rows("out", out, (torch.bfloat16,), n)
+    if out_rows != rows:
+        raise ValueError("out holds as many rows as x")
+    e4m3 = w.dtype == torch.float8_e4m3fn
+    if (x_scales is not None) != e4m3 or (w_scales is not None) != e4m3:
+        raise ValueError("e4m3 operands, and only they, come with x_scales and w_scales")
+    if e4m3:
+        _vector("x_scales", x_scales, rows, torch.float32)
+        _vector("w_scales", w_scales, groups * n, torch.float32)
+    _on(handle, stream)
+    purlin_grouped_matmul(handle, x, w, out, begin, count, groups, rows, n, k,
+                          PURLIN_E4M3 if e4m3 else PURLIN_BF16,
+                          PURLIN_WEIGHTS_KN if transposed else PURLIN_WEIGHTS_NK,
+                          x_scales=x_scales, w_scales=w_scales, ldx=ldx, ldw=ldw, ldy=ldy)
+    return out
+
+
+def grouped_matmul_weight_grad(dy, x, begin, count, handle, out=None, stream=None):
+    """groups x n x k gradients of the weights of :func:`grouped_matmul`."""
+    import torch
+
+    rows, n, lddy = _rows("dy", dy, (torch.bfloat16,))
+    x_rows, k, ldx = _rows("x", x, (torch.bfloat16,))
+    if x_rows != rows:
+        raise ValueError("dy and x hold the same rows")
+    groups = int(count.numel())
+    _groups(begin, count, groups)
+    if out is None:
+        out = torch.empty(groups, n, k, device=x.device, dtype=torch.bfloat16)
+    og, on, ok, lddw = _stack("out", out, (torch.bfloat16,))
+    if (og, on, ok) != (groups, n, k):
+        raise ValueError(f"out has shape {(og, on, ok)}, expected {(groups, n, k)}")
+    _on(handle, stream)
+    purlin_grouped_matmul_weight_grad(handle, dy, x, out, begin, count, groups, rows, n, k,
+                                      PURLIN_BF16, lddy=lddy, ldx=ldx, lddw=lddw)
+    return out
