@@ -23,6 +23,10 @@
 // before the row, and only the row's first and last windows go element by
 // element.  The grid is a multiple of the windows' elements, so all of a
 // block's rows have one phase and a thread's columns stay the same.
+//
+// Both are bound by bytes.  16384 x 7168 bf16 with a residual to e4m3: 134 us, 6.1
+// TB/s (91% of a copy's rate); backward of 32768 x 4096 bf16: 171 us, 6.3 TB/s.  A
+// single row of 4096 is a launch and one round trip to memory, 4.5 us on the device.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

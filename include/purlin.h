@@ -276,8 +276,10 @@ purlin_status purlin_noalloc_check(purlin_stream stream);
  * binary32; each output is rounded once.  Results do not depend on timing:
  * the same inputs give the same bits.  Partial results go to a workspace the
  * context owns, grown by the first call that needs more: during graph capture
- * such a call returns UNSUPPORTED, so make it once before.  rows, hidden, n
- * and k are at most 2^31 - 4096; offsets within a matrix may exceed 32 bits.  An
+ * such a call returns UNSUPPORTED, so make it once before (the first call of a
+ * kind also loads its kernel).  Launches overlap the end of the kernel before
+ * them on the stream, and touch no memory until it is done.  rows, hidden, n
+ * and k are at most 2^31 - 4096 (hidden: half that); offsets within a matrix may exceed 32 bits.  An
  * output may not overlap another buffer (ALIAS) except where stated. */
 
 /* Root-mean-square norm with the residual's addition, for each row:
