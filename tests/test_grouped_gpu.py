@@ -380,3 +380,68 @@ def test_graph_replay_with_counts_from_the_device(P):
             assert torch.equal(dw.view(-1, k), expected_grad(y0, x, begin.tolist(), counts)[:-1])
     finally:
         c.close()
+
+
+# Work enough for CTA pairs: rows x k x n of 8e9 and more, channels that fill 256.
+# Ragged and empty groups, tiles a row past a width, K blocks that end anywhere.
+PAIRS = [([1500, 0, 257, 1300], 1501, 2003), ([3, 2040, 513, 64, 1], 2056, 1792),
+         ([17] * 40 + [2500], 1024, 2560)]
+
+
+@pytest.mark.parametrize("layout", [0, 1], ids=["nk", "kn"])
+@pytest.mark.parametrize("counts,k,n", PAIRS, ids=["odd", "ragged", "small groups"])
+def test_pairs_whole_numbers(P, ctx, layout, counts, k, n):
+    begin, rows = packed(counts)
+    x = fill((rows, k), BF16, 30, True)
+    w = fill((len(counts), n, k) if layout == 0 else (len(counts), k, n), BF16, 31, True)
+    got = product(P, ctx, x, w, begin, counts, layout, ldy_pad=5)
+    assert torch.equal(got, expected(x, w, begin, counts, layout, ldy_pad=5))
+
+
+@pytest.mark.parametrize("counts,k,n", PAIRS, ids=["odd", "ragged", "small groups"])
+def test_pairs_whole_numbers_e4m3(P, ctx, counts, k, n):
+    begin, rows = padded(counts, max(counts) + 3)
+    x = fill((rows, k), E4M3, 32, True)
+    w = fill((len(counts), n, k), E4M3, 33, True)
+    xs = torch.full((rows,), math.nan, device="cuda")
+    for b, c in zip(begin, counts):
+        xs[b:b + c] = torch.exp2(torch.arange(c, device="cuda") % 5 - 2.0)
+    ws = torch.exp2(torch.arange(len(counts) * n, device="cuda").view(-1, n) % 7 - 3.0)
+    got = product(P, ctx, x, w, begin, counts, 0, xs, ws)
+    assert torch.equal(got, expected(x, w, begin, counts, 0, xs, ws))
+
+
+@pytest.mark.parametrize("counts,k,n", PAIRS, ids=["odd", "ragged", "small groups"])
+def test_pairs_weight_grad(P, ctx, counts, k, n):
+    """Rows outside the groups hold NaN and infinities: a pair cuts its last
+    stages in both CTAs."""
+    begin, rows = padded(counts, max(counts) + 9)
+    dy, x = fill((rows, n), BF16, 34, True), fill((rows, k), BF16, 35, True)
+    inside = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for b, c in zip(begin, counts):
+        inside[b:b + c] = True
+    dy[~inside] = math.nan
+    x[~inside] = math.inf
+    got = weight_grad(P, ctx, dy, x, begin, counts)
+    assert torch.equal(got, expected_grad(dy, x, begin, counts))
+    assert torch.equal(weight_grad(P, ctx, dy, x, begin, counts), got)
+
+
+def test_calls_in_a_row_on_one_stream(P, ctx):
+    """Launches overlap the end of the one before: each reads what it wrote."""
+    counts, k = [100, 0, 30, 200], 512
+    begin, rows = packed(counts)
+    x = fill((rows, k), BF16, 36, True)
+    w = torch.zeros(4, k, k, device="cuda", dtype=BF16)
+    perm = torch.randperm(k, generator=torch.Generator().manual_seed(1)).cuda()
+    w[:, torch.arange(k, device="cuda"), perm] = 1        # y[:, j] = x[:, perm[j]]
+    a, b = x.clone(), torch.empty_like(x)
+    for _ in range(20):
+        for s, d in ((a, b), (b, a)):
+            P.purlin_grouped_matmul(ctx, s, w, d, i64(begin), i64(counts), 4, rows, k, k,
+                                    P.PURLIN_BF16)
+    P.purlin_check(ctx)
+    want = x
+    for _ in range(40):
+        want = want[:, perm]
+    assert torch.equal(a, want)
