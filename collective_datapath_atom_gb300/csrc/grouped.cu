@@ -75,7 +75,7 @@ struct TcParams {
     const float *x_scales, *w_scales;
     const int64_t *begin, *count;
     float *partial;       // two accumulators a CTA
-    unsigned *arrived;    // two counters a CTA, zero between launches
+    unsigned *arrived;    // a counter a tile, CTA and writer, zero between launches
     size_t ldy;
     long long rows;
     int groups, ni, n, k;
@@ -95,6 +95,12 @@ struct Plan {
     long long left;                      // cost of those
     int bad;
 };
+
+// a / b of two that are not negative; 64-bit division is several times dearer, and
+// a decode step's numbers are small.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    return (unsigned long long)(a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
 // The group whose entry of a running total includes `at` (groups that add
 // nothing are skipped).
@@ -147,8 +153,8 @@ struct GroupTiles {
         return min(local, full) * full_cost + max(0, local - full) * rest_cost;
     }
     __device__ int tile_at(long long cost) const {
-        return cost < full * full_cost ? (int)(cost / full_cost)
-                                       : full + (int)((cost - full * full_cost) / rest_cost);
+        return cost < full * full_cost ? (int)divide(cost, full_cost)
+                                       : full + (int)divide(cost - full * full_cost, rest_cost);
     }
     __device__ int unit(int local) const { return block_cost(local < full ? width : rest); }
 };
@@ -175,6 +181,7 @@ __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool 
     }
     bad = __any_sync(0xffffffffu, bad);
     long long held = 0;
+    int most = 0;
     int down[kWidths] = {};   // row tiles at each width
     if (!bad) {
         unsigned low = 0, high = 0;
@@ -182,6 +189,7 @@ __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool 
             const int c = t.count[g];
             low += (unsigned)c & 0xFFFFu;
             high += (unsigned)c >> 16;
+            most = max(most, c);
             if constexpr (MODE != kGroupedGrad) {
 #pragma unroll
                 for (int w = 0; w < kWidths; ++w) down[w] += (c + 32 * w + 31) / (32 * w + 32);
@@ -189,6 +197,7 @@ __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool 
         }
         held = ((long long)__reduce_add_sync(0xffffffffu, high) << 16) +
                __reduce_add_sync(0xffffffffu, low);
+        most = __reduce_max_sync(0xffffffffu, most);
         bad = held > p.rows;
     }
     if (bad) {
@@ -201,27 +210,31 @@ __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool 
         }
         return;
     }
-    // the width that costs least, the wider of two that cost about the same
-    int mine = 0;
+    // the width that costs least, the wider of two that cost about the same; groups
+    // of a few rows leave no choice
+    int width = 32;
+    if (MODE == kGroupedGrad || most > 32) {
+        int mine = 0;
 #pragma unroll
-    for (int w = 0; w < kWidths; ++w) {
-        const int v = MODE == kGroupedGrad ? (p.n + 32 * w + 31) / (32 * w + 32) * p.groups
-                                           : __reduce_add_sync(0xffffffffu, down[w]);
-        if (lane == w) mine = v;
+        for (int w = 0; w < kWidths; ++w) {
+            const int v = MODE == kGroupedGrad ? (p.n + 32 * w + 31) / (32 * w + 32) * p.groups
+                                               : __reduce_add_sync(0xffffffffu, down[w]);
+            if (lane == w) mine = v;
+        }
+        unsigned key = 0xFFFFFFFFu;
+        if (lane < kWidths) {
+            const int w = 32 * lane + 32;
+            const float tiles = (float)mine * i_tiles;
+            const float blocks = MODE == kGroupedGrad
+                                     ? fmaxf(1.f, (float)held / (BK * (float)p.groups))
+                                     : (float)((p.k + BK - 1) / BK);
+            const float even = tiles / ctas, waves = ceilf(even);
+            const float cost = (even >= 1.f ? waves * blocks : fminf(blocks, even * blocks + kJoinBlocks)) *
+                                   block_clocks<CG>(w) + 12.f * w;
+            key = (__float_as_uint(cost) & ~7u) | (unsigned)(kWidths - 1 - lane);
+        }
+        width = 32 * (kWidths - (int)(__reduce_min_sync(0xffffffffu, key) & 7u));
     }
-    unsigned key = 0xFFFFFFFFu;
-    if (lane < kWidths) {
-        const int w = 32 * lane + 32;
-        const float tiles = (float)mine * i_tiles;
-        const float blocks = MODE == kGroupedGrad
-                                 ? fmaxf(1.f, (float)held / (BK * (float)p.groups))
-                                 : (float)((p.k + BK - 1) / BK);
-        const float even = tiles / ctas, waves = ceilf(even);
-        const float cost = (even >= 1.f ? waves * blocks : fminf(blocks, even * blocks + kJoinBlocks)) *
-                               block_clocks<CG>(w) + 12.f * w;
-        key = (__float_as_uint(cost) & ~7u) | (unsigned)(kWidths - 1 - lane);
-    }
-    const int width = 32 * (kWidths - (int)(__reduce_min_sync(0xffffffffu, key) & 7u));
     int tiles = 0;
     long long spent = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
@@ -256,7 +269,7 @@ __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool 
     // 2048 x 7168 x 2048 took 99 us instead of 65.)
     const long long idle = ctas - tiles;
     const bool cut = tiles > 0 && idle > 0 &&
-                     idle * (spent / tiles) >= (long long)kJoinBlocks * ctas * block_cost(width);
+                     idle * spent >= (long long)kJoinBlocks * ctas * block_cost(width) * tiles;
     t.whole = cut ? 0 : tiles;
     t.left = cut ? spent : 0;
     // at least four of the dearest blocks a run: a block begins in each
@@ -274,7 +287,6 @@ struct TcShared {
     uint64_t done[2], free[2];    // accumulator complete; accumulator read
     uint64_t drain;
     uint32_t tmem;
-    int last;
     alignas(16) __nv_bfloat16 turn[kWriters][16 * 32];   // 16 rows of 32 channels a warp
     float row_scales[2][kTileJ];                         // of the tile at hand, and the next
 };
@@ -291,10 +303,10 @@ struct Unit {
 };
 
 // The runs split the cost evenly; a block belongs to the run it begins in.
-__device__ __forceinline__ long long run_begin(const Plan &t, int c) { return t.left * c / t.runs; }
+__device__ __forceinline__ long long run_begin(const Plan &t, int c) { return divide(t.left * c, t.runs); }
 
 __device__ __forceinline__ int run_of(const Plan &t, long long at) {
-    return (int)(((at + 1) * t.runs - 1) / t.left);
+    return (int)divide((at + 1) * t.runs - 1, t.left);
 }
 
 // Walks the units of one CTA (or pair) `c` of `ctas`.
@@ -330,8 +342,8 @@ struct Walk {
             const int local = of.tile_at(at - t.cost[q.g]), unit = of.unit(local);
             q.tile = t.tiles[q.g] + local;
             const long long begin = t.cost[q.g] + of.before(local);
-            q.kb0 = (int)((at - begin + unit - 1) / unit);
-            q.kb1 = (int)min((long long)of.blocks, (end - begin + unit - 1) / unit);
+            q.kb0 = (int)divide(at - begin + unit - 1, unit);
+            q.kb1 = (int)min((long long)of.blocks, divide(end - begin + unit - 1, unit));
             at = begin + (long long)of.blocks * unit;
             if (q.kb0 >= q.kb1) continue;   // the run begins inside the tile's last block
             q.c0 = run_of(t, begin);
@@ -601,7 +613,7 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
         // on the row: eight rows of one piece, and four pieces of a row, meet no bank twice
         auto piece = [&](int r, int k) { return turn + r * 64 + ((k ^ (r >> 1)) & 3) * 16; };
         uint32_t acc = 0, tile = 0;
-        bool dead = false;   // a wait expired: walk on, for the barriers of the writers
+        bool dead = false;   // a wait expired: walk on, for the writers' barriers and counters
         while (walk.next(q)) {
             const int i0 = q.i0 + rank * kTileI + quarter * 32;   // the warp's first channel
             const bool shared = q.c0 != q.c1;
@@ -727,17 +739,19 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                                                __uint_as_float(r[4 * x + 2]),
                                                __uint_as_float(r[4 * x + 3])));
                 }
-                // the last of the tile's CTAs adds the accumulators in K order
+                // Warp by warp: the tile's last CTA to get here adds the accumulators, in K
+                // order.  Nothing but this warp's counterparts to wait for.
                 __threadfence();
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
-                if (warp == 2 && lane == 0) {
-                    unsigned *n = p.arrived + (size_t)q.tile * CG + rank;
-                    s.last = atomicAdd(n, 1u) == (unsigned)(q.c1 - q.c0);
-                    if (s.last) *n = 0;
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    unsigned *n = p.arrived + ((size_t)q.tile * CG + rank) * kWriters + warp - 2;
+                    last = atomicAdd(n, 1u) == (unsigned)(q.c1 - q.c0);
+                    if (last) *n = 0;
                 }
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
-                if (s.last) __threadfence();
-                for (int c = c_first; c < q.nj && !dead && s.last; c += kColStep) {
+                last = __shfl_sync(0xffffffffu, last, 0);
+                if (last) __threadfence();
+                for (int c = c_first; c < q.nj && !dead && last; c += kColStep) {
                     float4 sum[4] = {};
                     for (int k = q.c0; k <= q.c1; k += 3) {
                         float4 u[3][4];   // three runs' loads in flight
@@ -767,8 +781,6 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                     }
                     put(c, r);
                 }
-                // s.last is free again
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kWriters) : "memory");
             } else if (!dead) {
                 // the next 16 columns are on their way while these are written
                 fetch(c_first, ahead);

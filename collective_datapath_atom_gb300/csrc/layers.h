@@ -80,7 +80,7 @@ struct GroupedArgs {
 };
 
 constexpr int kMaxGroups = PURLIN_MAX_GROUPS;
-constexpr int kJoinCounters = 2048;          // two an SM
+constexpr int kJoinCounters = 16384;         // eight writers a CTA, 2048 CTAs
 constexpr size_t kGroupedRowTile = 32;       // the narrowest tile's rows, and its channels
 constexpr size_t kGroupedChannelTile = 128;
 
