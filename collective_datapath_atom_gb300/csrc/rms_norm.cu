@@ -209,6 +209,9 @@ __device__ __forceinline__ Window<T, V> read_weight(const T *w, int e, int hidde
 constexpr int norm_threads(int held) { return held <= 8 ? 1024 : 512; }
 constexpr int kBackwardThreads = 512, kStagedThreads = 512;
 constexpr int kShortRows = 8;   // rows of a block with a warp a row
+// Backward, fewer rows a block and fewer blocks: less to join (4000 x 768 bf16 16.6
+// us, with 8 rows and 1024 threads an SM 32.1; 32768 x 512 31.1 and 39.2).
+constexpr int kBackwardShortRows = 4, kBackwardThreadsSm = 512;
 
 // A thread holds ITEMS windows of V elements of its row.  blockDim.y rows a
 // block; more than one only where blockDim.x is one warp.  Up to 64 bytes a
@@ -863,7 +866,7 @@ unsigned warps_of(size_t windows, int items) {
 // threads allow, which is the quickest for a block's first row.
 template <int V, typename F>
 Shape register_shape(size_t rows, size_t hidden, bool edge, int most_items, int sms,
-                     int short_rows, F threads) {
+                     int short_rows, int threads_sm, F threads) {
     Shape s;
     const size_t windows = windows_of<V>(hidden, edge);
     // a warp a row as soon as it can hold one: many short rows
@@ -878,9 +881,9 @@ Shape register_shape(size_t rows, size_t hidden, bool edge, int most_items, int 
     if (s.items == 0) return s;
     while (s.items > 1 && warps_of(windows, s.items / 2) == s.tx) s.items /= 2;
     s.ty = s.tx == 32 ? (unsigned)short_rows : 1;
-    // about 1024 threads an SM; a multiple of the windows' elements, so that a
-    // block's rows share their phase, or a row a block
-    const size_t blocks = std::max<size_t>(1, 1024 / (s.tx * s.ty));
+    // a multiple of the windows' elements, so that a block's rows share their phase,
+    // or a row a block
+    const size_t blocks = std::max<size_t>(1, threads_sm / (s.tx * s.ty));
     const size_t grid = std::max<size_t>((size_t)sms * blocks / V * V, V);
     s.grid = (unsigned)std::min<size_t>((rows + s.ty - 1) / s.ty, grid);
     return s;
@@ -900,7 +903,9 @@ Shape staged_shape(size_t rows, size_t hidden, bool edge, int arrays, int sms, b
     const size_t threads_sm = edge ? 640 : 448;   // edges take more instructions a row
     const size_t windows = windows_of<V>(hidden, edge);
     const size_t stage = (hidden + 2 * (V - 1)) / V * 16 * (size_t)arrays;   // as RowRing has it
-    if (V == 1 || windows <= 128) return s;
+    // a row that fits a warp's registers stays there; backward, where dweight's sums
+    // need them, less of one does (32768 x 1024 bf16 55.7 us, from registers 60.8)
+    if (V == 1 || windows <= (late ? 100 : 128)) return s;
     const int items = warps_of(windows, 4) <= (unsigned)kStagedThreads ? 4 : 8;
     const unsigned tx = warps_of(windows, items);
     if (items * V > 32 || tx > (unsigned)kStagedThreads) return s;
@@ -953,7 +958,7 @@ cudaError_t norm_typed(const NormArgs &a, NormParams &p) {
         }
     }
     constexpr int kMost = std::min(8, 32 / V);
-    const Shape s = register_shape<V>(a.rows, a.hidden, EDGE, kMost, a.sms, kShortRows,
+    const Shape s = register_shape<V>(a.rows, a.hidden, EDGE, kMost, a.sms, kShortRows, 1024,
                                       [](int items) { return norm_threads(items * V); });
     const dim3 block(s.tx, s.ty);
     if (s.items == 1) norm_kernel<T, O, V, 1, EDGE><<<s.grid, block, 0, a.stream>>>(p);
@@ -1004,8 +1009,10 @@ BackwardShape backward_shape(const NormBackwardArgs &a) {
     if (s.windows) base = staged_shape<V>(a.rows, a.hidden, s.edge, a.dtotal ? 3 : 2, a.sms, true);
     if (s.items != 4)   // eight windows a thread are too many here: dweight's sums and the weight
         base = s.windows
-                   ? register_shape<V>(a.rows, a.hidden, s.edge, 4, a.sms, kShortRows, threads)
-                   : register_shape<1>(a.rows, a.hidden, false, 4, a.sms, kShortRows, threads);
+                   ? register_shape<V>(a.rows, a.hidden, s.edge, 4, a.sms, kBackwardShortRows,
+                                       kBackwardThreadsSm, threads)
+                   : register_shape<1>(a.rows, a.hidden, false, 4, a.sms, kBackwardShortRows,
+                                       kBackwardThreadsSm, threads);
     if (s.items == 0)
         s.grid = (unsigned)std::max<size_t>(1, std::min<size_t>(a.rows, (size_t)a.sms * 2));
     return s;
