@@ -27,8 +27,8 @@
 //
 // Bound by the tensor cores at prefill sizes: 16384 x 7168 x 2048 bf16 in one
 // group takes 276 us (1.74 PFLOP/s, the card at its power limit; one cuBLAS product
-// 285), over 8 Zipf groups 280 us in a short burst and 312 in a long one, the
-// tensor pipe 79% active; e4m3 at twice the channels 277 and 317 (3.5 and 3.0
+// 285), over 8 Zipf groups 280 us in a short burst and 316 in a long one, the
+// tensor pipe 79% active; e4m3 at twice the channels 272 and 319 (3.5 and 3.0
 // PFLOP/s); data gradient 260, weight gradient 294 us.  Bound by the weights' bytes
 // at decode sizes: 8 rows on 5 of 8 experts, 147 MB, 31 us; 128 rows on 64
 // experts, e4m3, 269 MB, 47 us (5.7 TB/s), of which about 5 us are the launch, the

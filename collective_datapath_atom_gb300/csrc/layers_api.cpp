@@ -43,6 +43,11 @@ bool overlap(const Matrix &a, const Matrix &b) {
     return !(d >= a.width && d + b.width <= a.pitch);
 }
 
+// A device array of one int64 a group.
+Matrix group_array(const int64_t *p, int groups) {
+    return matrix(p, 1, 2 * (size_t)groups, 2 * (size_t)groups, PURLIN_F32);
+}
+
 // The same elements in the same places: allowed where a thread reads an
 // element before it writes it.
 bool same(const Matrix &a, const Matrix &b) {
@@ -291,7 +296,8 @@ purlin_status purlin_grouped_matmul(purlin_ctx *ctx, const void *x, size_t ldx, 
     if (overlap(my, matrix(x, rows, k, ldx, dtype)) ||
         overlap(my, matrix(w, (size_t)groups * w_rows, w_cols, ldw, dtype)) ||
         overlap(my, matrix(x_scales, 1, rows, rows, PURLIN_F32)) ||
-        overlap(my, matrix(w_scales, 1, (size_t)groups * n, (size_t)groups * n, PURLIN_F32)))
+        overlap(my, matrix(w_scales, 1, (size_t)groups * n, (size_t)groups * n, PURLIN_F32)) ||
+        overlap(my, group_array(begin, groups)) || overlap(my, group_array(count, groups)))
         return PURLIN_ERR_ALIAS;
     if (too_many_tiles(n, rows, 1, groups) || too_long(w_rows, ldw, es))
         return PURLIN_ERR_UNSUPPORTED;
@@ -342,7 +348,8 @@ purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy,
         return PURLIN_ERR_ALIGNMENT;
     const Matrix mw = matrix(dw, (size_t)groups * n, k, lddw, dtype);
     if (overlap(mw, matrix(dy, rows, n, lddy, dtype)) ||
-        overlap(mw, matrix(x, rows, k, ldx, dtype)))
+        overlap(mw, matrix(x, rows, k, ldx, dtype)) || overlap(mw, group_array(begin, groups)) ||
+        overlap(mw, group_array(count, groups)))
         return PURLIN_ERR_ALIAS;
     if (too_many_tiles(k, 0, n / kGroupedRowTile + 1, groups)) return PURLIN_ERR_UNSUPPORTED;
     if (ctx == nullptr) return PURLIN_ERR_INVALID_ARG;

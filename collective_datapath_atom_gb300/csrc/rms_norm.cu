@@ -1049,7 +1049,7 @@ cudaError_t norm_backward_any(const NormBackwardArgs &a) {
                           : s.edge   ? norm_backward_typed<T, V, true>(a, p, s)
                                      : norm_backward_typed<T, V, false>(a, p, s);
     if (e != cudaSuccess) return e;
-    // the join's launch overlaps the rows' kernel (8.9 against 12.0 us at 509 x 1021 f32)
+    // the join's launch overlaps the rows' kernel (3 us less at 509 x 1021 f32)
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)((a.hidden + 31) / 32));
     c.blockDim = dim3(32, kJoinRows);

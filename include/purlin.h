@@ -347,7 +347,8 @@ typedef enum {
  * bytes.  rows, n or groups == 0 is a no-op.
  * Errors: INVALID_ARG (NULL, groups out of 0..PURLIN_MAX_GROUPS, k 0, ld too
  * small, scales given or missing), UNSUPPORTED (F32; E4M3 with KN; more than
- * 2^31 tiles), ALIGNMENT, ALIAS (y and an input), OOM, CUDA. */
+ * 2^30 tiles), ALIGNMENT, ALIAS (y and an input, begin and count
+ * among them), OOM, CUDA. */
 purlin_status purlin_grouped_matmul(purlin_ctx *ctx, const void *x, size_t ldx, const void *w,
                                     size_t ldw, void *y, size_t ldy, const float *x_scales,
                                     const float *w_scales, const int64_t begin[],

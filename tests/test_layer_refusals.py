@@ -99,6 +99,7 @@ def test_backward_refusals(P, kw, want):
     (dict(dtype=2, x_scales=F + 2, w_scales=F + 4096), ALIGNMENT),
     (dict(y=A), ALIAS), (dict(y=B + 64), ALIAS), (dict(y=A - 2), ALIAS),
     (dict(dtype=2, x_scales=C, w_scales=F), ALIAS),
+    (dict(begin=C + 8), ALIAS), (dict(count=C + 248), ALIAS),
 ])
 def test_product_refusals(P, kw, want):
     assert product(P, **kw) == want
@@ -108,7 +109,8 @@ def test_product_refusals(P, kw, want):
     (dict(dtype=0), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED), (dict(dtype=9), INVALID),
     (dict(dy=A + 4), ALIGNMENT), (dict(x=B + 4), ALIGNMENT), (dict(dw=C + 1), ALIGNMENT),
     (dict(lddy=33), ALIGNMENT), (dict(k=65), ALIGNMENT),
-    (dict(dw=A), ALIAS), (dict(dw=B + 2), ALIAS),
+    (dict(dw=A), ALIAS), (dict(dw=B + 2), ALIAS), (dict(begin=C + 8), ALIAS),
+    (dict(count=C), ALIAS),
 ])
 def test_grad_refusals(P, kw, want):
     assert grad(P, **kw) == want
