@@ -563,12 +563,14 @@ struct NormBackwardParams {
 };
 
 // blockDim.y rows a block, more than one only where blockDim.x is one warp: then
-// the warps' shares of dweight are added up in shared memory, warp by warp.
-template <typename T, int V, int ITEMS, bool EDGE>
-__global__ void __launch_bounds__(kBackwardThreads)
+// the warps' shares of dweight are added up in shared memory, warp by warp.  WIDE:
+// blocks of up to 1024 threads, with registers for a row and dweight's sums but not
+// for the weight, which every row reads again.
+template <typename T, int V, int ITEMS, bool EDGE, bool WIDE = false>
+__global__ void __launch_bounds__(WIDE ? 1024 : kBackwardThreads)
 norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
-    constexpr bool AHEAD = ITEMS * V * sizeof(T) <= 32;
+    constexpr bool AHEAD = !WIDE && ITEMS * V * sizeof(T) <= 32;
     __shared__ float sums[2][2][32];   // rows take turns: one barrier a row
     __shared__ float joined[32 * ITEMS * V];
     const int hidden = (int)p.hidden;
@@ -587,15 +589,19 @@ norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
             gk[i] = read_window<T, V, EDGE>(dy, e0 + i * estep, hidden);
             tk[i] = read_window<T, V, EDGE>(t, e0 + i * estep, hidden);
         }
-        if (p.dtotal) {
+        if (!WIDE && p.dtotal) {
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) dk[i] = read_window<T, V, EDGE>(d, e0 + i * estep, hidden);
         }
     };
     if (row < p.rows) fetch(row);
+    auto weight = [&](int i) {
+        return read_weight<T, V, EDGE>(static_cast<const T *>(p.weight), e0 + i * estep, hidden);
+    };
+    if constexpr (!WIDE) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-        wk[i] = read_weight<T, V, EDGE>(static_cast<const T *>(p.weight), e0 + i * estep, hidden);
+        for (int i = 0; i < ITEMS; ++i) wk[i] = weight(i);
+    }
     const int warps = blockDim.x >> 5;
     int turn = 0;
     for (; row < p.rows; row += step, turn ^= 1) {   // one row a warp, or all of the block's one
@@ -606,6 +612,7 @@ norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
             g[i] = gk[i];
             t[i] = tk[i];
             d[i] = dk[i];
+            if constexpr (WIDE) wk[i] = weight(i);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float u = t[i].at(j);
@@ -640,6 +647,12 @@ norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             float o[V];
+            if constexpr (WIDE) {
+                wk[i] = weight(i);
+                if (p.dtotal)
+                    d[i] = read_window<T, V, EDGE>(static_cast<const T *>(p.dtotal) + row * p.lddt,
+                                                   e0 + i * estep, hidden);
+            }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float u = t[i].at(j), y = g[i].at(j);
@@ -991,7 +1004,7 @@ cudaError_t norm_any(const NormArgs &a) {
 
 // A backward launch: its shape, and whether it takes windows and meets edges.
 struct BackwardShape : Shape {
-    bool windows = false, edge = false;
+    bool windows = false, edge = false, wide = false;
 };
 
 template <typename T>
@@ -1013,14 +1026,29 @@ BackwardShape backward_shape(const NormBackwardArgs &a) {
                                        kBackwardThreadsSm, threads)
                    : register_shape<1>(a.rows, a.hidden, false, 4, a.sms, kBackwardShortRows,
                                        kBackwardThreadsSm, threads);
-    if (s.items == 0)
+    const unsigned most = s.windows ? warps_of(windows_of<V>(a.hidden, s.edge), 4) : 2048;
+    if (s.items == 0 && V == 4 && most <= 1024) {
+        // rows of 8192 to 16384 f32: a block an SM (3000 x 16384 186 us, read again from
+        // the L2 cache 312)
+        s.wide = true;
+        s.items = 4;
+        s.tx = most;
+        s.grid = (unsigned)std::min<size_t>(a.rows, std::max<size_t>(a.sms / V * V, V));
+    } else if (s.items == 0) {
         s.grid = (unsigned)std::max<size_t>(1, std::min<size_t>(a.rows, (size_t)a.sms * 2));
+    }
     return s;
 }
 
 template <typename T, int V, bool EDGE>
 cudaError_t norm_backward_typed(const NormBackwardArgs &a, const NormBackwardParams &p,
-                                const Shape &s) {
+                                const BackwardShape &s) {
+    if constexpr (V == 4) {
+        if (s.wide) {
+            norm_backward_kernel<T, V, 4, EDGE, true><<<s.grid, s.tx, 0, a.stream>>>(p);
+            return cudaGetLastError();
+        }
+    }
     if constexpr (V > 1) {
         if (s.stages > 0) {
             static const cudaError_t ready = prepared(norm_backward_staged_kernel<T, V, 4, EDGE>);
