@@ -24,8 +24,8 @@
 // element.  The grid is a multiple of the windows' elements, so all of a
 // block's rows have one phase and a thread's columns stay the same.
 //
-// Both are bound by bytes.  16384 x 7168 bf16 with a residual to e4m3: 134 us, 6.1
-// TB/s (91% of a copy's rate); backward of 32768 x 4096 bf16: 171 us, 6.3 TB/s.  A
+// Both are bound by bytes.  16384 x 7168 bf16 with a residual to e4m3: 124 us, 6.6
+// TB/s (99% of a copy's rate); backward of 32768 x 4096 bf16: 171 us, 6.3 TB/s.  A
 // single row of 4096 is a launch and one round trip to memory, 4.5 us on the device.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -40,7 +40,8 @@ namespace purlin {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
-constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126: its reciprocal is finite
+constexpr float kF32Max = 3.40282347e38f;      // the largest finite value
+constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126, the smallest normal value
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -92,6 +93,40 @@ __device__ __forceinline__ void store(O *p, const float (&in)[V]) {
         if constexpr (V == 4) *reinterpret_cast<uint32_t *>(p) = w[0];
         else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
+}
+
+// v / d from the reciprocal of d (rounded to nearest): the product, and one step
+// with its exact remainder (P. Markstein, IBM J. Res. Dev. 34, 1990).  The product
+// alone can be off by an ulp either way, which moves ties.  16384 x 7168 to e4m3:
+// a division an element 229 us, this 124 (the product alone 135: the reads run
+// further ahead of the writes).
+__device__ __forceinline__ float quotient(float v, float d, float inv) {
+    const float q = v * inv;
+    return fmaf(fmaf(-q, d, v), inv, q);
+}
+
+// The mean of n values from their sum, inv = 1 / n; an infinite sum stays one.
+__device__ __forceinline__ float mean_of(float sum, float n, float inv) {
+    return fabsf(sum) <= kF32Max ? quotient(sum, n, inv) : sum;
+}
+
+// A row's values v over its e4m3 scale.
+template <int ITEMS, int V>
+__device__ __forceinline__ void divide_row(float (&v)[ITEMS][V], float scale) {
+    // tiny rows: remainders would fall below the smallest value; both by 2^64, exactly
+    if (scale < 0x1p-80f) {
+        scale *= 0x1p64f;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] *= 0x1p64f;
+    }
+    const float inv = 1.f / scale;
+    const float d = scale <= kF32Max ? scale : 0.f;   // infinite: the products, 0 or NaN, stand
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = quotient(v[i][j], d, inv);
 }
 
 struct Sum {
@@ -284,13 +319,9 @@ norm_kernel(const __grid_constant__ NormParams p) {
             // fmaxf passes over NaN: the scale stays a number, the elements are NaN
             const float scale =
                 fmaxf(reduce_row<Max>(most, warp_only, maxes[turn]) / kE4m3Max, kScaleMin);
-            const float inv = 1.f / scale;
+            divide_row(t, scale);
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) t[i][j] *= inv;
-                write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
-            }
+            for (int i = 0; i < ITEMS; ++i) write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
             if (threadIdx.x == 0) p.scales[row] = scale;
         }
         if constexpr (!AHEAD) {
@@ -456,7 +487,7 @@ norm_staged_kernel(const __grid_constant__ NormParams p) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
         weight.put(i, read_weight<T, V, EDGE>(static_cast<const T *>(p.weight), e0 + i * estep, hidden));
-    const float inv_hidden = 1.f / (float)hidden;   // one more rounding of the mean, no division a row
+    const float inv_hidden = 1.f / (float)hidden;
     uint32_t n = 0;
     for (size_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++n, ring.next()) {
         ring.wait(p.err);
@@ -482,7 +513,7 @@ norm_staged_kernel(const __grid_constant__ NormParams p) {
             for (int i = 0; i < ITEMS; ++i) write_window<T, V, EDGE>(total, e0 + i * estep, hidden, t[i]);
         }
         const float r =
-            rsqrtf(reduce_row<Sum>(ss, false, sums[n & 1]) * inv_hidden + p.eps);
+            rsqrtf(mean_of(reduce_row<Sum>(ss, false, sums[n & 1]), (float)hidden, inv_hidden) + p.eps);
         if (threadIdx.x == 0) ring.issue();   // the sum's barrier: every thread has read its share
         O *y = static_cast<O *>(p.y) + row * p.ldy;
         float most = 0.f;
@@ -500,13 +531,9 @@ norm_staged_kernel(const __grid_constant__ NormParams p) {
             // fmaxf passes over NaN: the scale stays a number, the elements are NaN
             const float scale =
                 fmaxf(reduce_row<Max>(most, false, maxes[n & 1]) / kE4m3Max, kScaleMin);
-            const float inv = 1.f / scale;
+            divide_row(t, scale);
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) t[i][j] *= inv;
-                write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
-            }
+            for (int i = 0; i < ITEMS; ++i) write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
             if (threadIdx.x == 0) p.scales[row] = scale;
         }
     }
@@ -532,20 +559,20 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
         ss = fmaf(t, t, ss);
     }
     const float r = rsqrtf(reduce_row<Sum>(ss, false, sums) / (float)p.hidden + p.eps);
-    float inv = 1.f;
+    float scale = 1.f;
     if constexpr (sizeof(O) == 1) {
         float most = 0.f;
         for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x)
             most = fmaxf(most, fabsf(at(e) * r * to_f32<T>(w[e])));
-        const float scale = fmaxf(reduce_row<Max>(most, false, maxes) / kE4m3Max, kScaleMin);
-        inv = 1.f / scale;
+        scale = fmaxf(reduce_row<Max>(most, false, maxes) / kE4m3Max, kScaleMin);
         if (threadIdx.x == 0) p.scales[row] = scale;
     }
     for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
         // total may be x or the residual itself: each element is read before it is written
         const float t = at(e);
         if (p.total) static_cast<T *>(p.total)[row * p.ldt + e] = from_f32<T>(t);
-        y[e] = from_f32<O>(t * r * to_f32<T>(w[e]) * inv);
+        const float v = t * r * to_f32<T>(w[e]);
+        y[e] = from_f32<O>(sizeof(O) == 1 ? v / scale : v);
     }
 }
 
@@ -640,9 +667,11 @@ norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
                 gt += sums[turn][1][k];
             }
         }
-        const float inv_n = 1.f / (float)p.hidden;
+        const float inv_hidden = 1.f / (float)p.hidden;
+        // (a division here: without its call the compiler keeps the row unpacked over the
+        // sums, and four windows of bf16 spill 500 bytes)
         const float r = rsqrtf(tt / (float)p.hidden + p.eps);
-        const float c = r * r * (gt * inv_n);
+        const float c = r * r * mean_of(gt, (float)p.hidden, inv_hidden);
         T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -657,7 +686,7 @@ norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
             for (int j = 0; j < V; ++j) {
                 const float u = t[i].at(j), y = g[i].at(j);
                 acc[i][j] = fmaf(y, u * r, acc[i][j]);
-                o[j] = r * (y * wk[i].at(j) - u * c);
+                o[j] = r * fmaf(y, wk[i].at(j), -(u * c));
                 if (p.dtotal) o[j] += d[i].at(j);
             }
             write_window<T, V, EDGE>(dx, e0 + i * estep, hidden, o);
@@ -758,8 +787,8 @@ norm_backward_staged_kernel(const __grid_constant__ NormBackwardParams p) {
             tt += sums[n & 1][0][k];
             gt += sums[n & 1][1][k];
         }
-        const float r = rsqrtf(tt * inv_hidden + p.eps);
-        const float c = r * r * (gt * inv_hidden);
+        const float r = rsqrtf(mean_of(tt, (float)hidden, inv_hidden) + p.eps);
+        const float c = r * r * mean_of(gt, (float)hidden, inv_hidden);
         T *dx = static_cast<T *>(p.dx) + row * p.lddx;
         // the row is read again rather than held: the registers go to dweight's sums
 #pragma unroll
@@ -774,7 +803,7 @@ norm_backward_staged_kernel(const __grid_constant__ NormBackwardParams p) {
             for (int j = 0; j < V; ++j) {
                 const float u = t.at(j), y = g.at(j);
                 acc[i][j] = fmaf(y, u * r, acc[i][j]);
-                o[j] = r * (y * wk.at(j) - u * c);
+                o[j] = r * fmaf(y, wk.at(j), -(u * c));
                 if (p.dtotal) o[j] += d.at(j);
             }
             write_window<T, V, EDGE>(dx, e0 + i * estep, hidden, o);
@@ -816,7 +845,7 @@ norm_backward_long_kernel(const __grid_constant__ NormBackwardParams p) {
         const float c = r * r * (gt / (float)p.hidden);
         for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
             const float u = to_f32<T>(t[e]), d = to_f32<T>(dy[e]);
-            float o = r * (d * to_f32<T>(w[e]) - u * c);
+            float o = r * fmaf(d, to_f32<T>(w[e]), -(u * c));
             if (p.dtotal) o += to_f32<T>(static_cast<const T *>(p.dtotal)[row * p.lddt + e]);
             static_cast<T *>(p.dx)[row * p.lddx + e] = from_f32<T>(o);
             partial[e] = fmaf(d, u * r, partial[e]);

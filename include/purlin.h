@@ -286,8 +286,8 @@ purlin_status purlin_noalloc_check(purlin_stream stream);
  *   t = x + residual   (residual NULL: t = x)
  *   v = t / sqrt(mean(t^2) + eps) * weight
  * out_dtype == dtype: y = v, and scales must be NULL.  out_dtype E4M3:
- * scales[row] = max(max |v| / 448, 2^-126) and y = v / scales[row] in e4m3
- * (nearest even; the maximum skips NaN, and a NaN element is e4m3 NaN).  An
+ * scales[row] = max(max |v| / 448, 2^-126) and y = v / scales[row], a binary32
+ * quotient, in e4m3 (nearest even; the maximum skips NaN, and a NaN element is e4m3 NaN).  An
  * all-zero row gives zeros.  total (or NULL) receives t: the residual stream
  * of the next layer.  The norm is of the unrounded t.
  * dtype F32 or BF16, that of x, residual, weight and total.  Pointers need
