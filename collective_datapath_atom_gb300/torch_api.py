@@ -182,6 +182,9 @@ def _rows(name, t, dtypes, cols=None):
     """(rows, cols, row stride) of a CUDA matrix whose rows are contiguous."""
     if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
+    # (an expanded view's stride of 0 would read as "contiguous" below)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: its rows overlap (strides {t.stride()}); expanded views need a copy")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if cols is not None and t.shape[1] != cols:
@@ -261,6 +264,8 @@ def _stack(name, t, dtypes):
     if not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or \
             (t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1)):
         raise ValueError(f"{name} must be CUDA matrices with contiguous rows, one after another")
+    if t.shape[0] * t.shape[1] > 1 and t.stride(1) < t.shape[2]:
+        raise ValueError(f"{name}: its rows overlap (strides {t.stride()}); expanded views need a copy")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     return (*t.shape, t.stride(1))
