@@ -782,16 +782,14 @@ grouped_tc_kernel(const __grid_constant__ TcParams p) {
                     put(c, r);
                 }
             } else if (!dead) {
-                // the next 16 columns are on their way while these are written
-                fetch(c_first, ahead);
-#pragma unroll 1
-                for (int c = c_first; c < q.nj; c += kColStep) {
-                    tensor::tmem_wait_loads(ahead);
+                tensor::walk_columns(
+                    c_first, kColStep, q.nj, [&](int c) { fetch(c, ahead); },
+                    [&] {
+                        tensor::tmem_wait_loads(ahead);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) r[x] = ahead[x];
-                    if (c + kColStep < q.nj) fetch(c + kColStep, ahead);
-                    put(c, r);
-                }
+                        for (int x = 0; x < 16; ++x) r[x] = ahead[x];
+                    },
+                    [&](int c) { put(c, r); });
             }
             if (!empty && !dead) {
                 tensor::fence_before_sync();

@@ -155,6 +155,24 @@ __device__ __forceinline__ void tmem_wait_loads(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// Columns first, first + step, ... below `end` of an accumulator: the loads of the
+// next ones are on their way while those that `wait` handed over are put away.
+// Every load issued is waited for: one that is not may land in registers that hold
+// something else by then, or read an accumulator that is given up already.  A warp
+// without columns (a tile of 16 rows leaves half of them none) issues no load.
+template <typename Fetch, typename Wait, typename Put>
+__device__ __forceinline__ void walk_columns(int first, int step, int end, Fetch fetch, Wait wait,
+                                             Put put) {
+    if (first >= end) return;
+    fetch(first);
+#pragma unroll 1
+    for (int c = first; c < end; c += step) {
+        wait();
+        if (c + step < end) fetch(c + step);
+        put(c);
+    }
+}
+
 // Four 8 x 8 matrices of 16-bit fragments, transposed: thread 8 m + i gives the
 // address of 16 bytes for column i of matrix m.
 __device__ __forceinline__ void store_transposed(uint32_t smem, uint32_t a, uint32_t b, uint32_t c,
