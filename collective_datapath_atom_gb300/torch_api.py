@@ -178,6 +178,15 @@ def all_to_all_v(xs, outs, counts, handle, stream=None):
 
 # ------------------------------------------------------- layer operators ---
 
+def _pitch(t, rows, stride):
+    """Row stride to pass on for `rows` rows.  A single row's may be anything; it is
+    rounded up to 16 bytes, which the products ask of a matrix's rows."""
+    if rows > 1:
+        return stride
+    per = 16 // t.element_size()
+    return (t.shape[-1] + per - 1) // per * per
+
+
 def _rows(name, t, dtypes, cols=None):
     """(rows, cols, row stride) of a CUDA matrix whose rows are contiguous."""
     if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
@@ -189,7 +198,7 @@ def _rows(name, t, dtypes, cols=None):
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if cols is not None and t.shape[1] != cols:
         raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
-    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.shape[0], t.shape[1], _pitch(t, t.shape[0], t.stride(0))
 
 
 def _vector(name, t, n, dtype):
@@ -261,14 +270,16 @@ def rms_norm_backward(dy, total, weight, handle, dtotal=None, dx=None, dweight=N
 
 def _stack(name, t, dtypes):
     """(groups, rows, cols, row stride) of matrices that lie one after another."""
-    if not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or \
-            (t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1)):
+    if not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be CUDA matrices with contiguous rows")
+    row = t.stride(1) if t.shape[1] > 1 else t.stride(0)   # one row a matrix: from group to group
+    if t.shape[0] > 1 and t.stride(0) != t.shape[1] * row:
         raise ValueError(f"{name} must be CUDA matrices with contiguous rows, one after another")
-    if t.shape[0] * t.shape[1] > 1 and t.stride(1) < t.shape[2]:
+    if t.shape[0] * t.shape[1] > 1 and row < t.shape[2]:
         raise ValueError(f"{name}: its rows overlap (strides {t.stride()}); expanded views need a copy")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return (*t.shape, t.stride(1))
+    return (*t.shape, _pitch(t, t.shape[0] * t.shape[1], row))
 
 
 def _groups(begin, count, groups):

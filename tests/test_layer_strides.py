@@ -122,3 +122,71 @@ def test_pitched_rows_pass_with_their_stride(T):
     grad(T, x=wide)
     assert T.calls[0][2]["ldx"] == T.calls[0][2]["ldt"] == 80
     assert T.calls[1][2]["lddt"] == T.calls[2][2]["ldx"] == T.calls[3][2]["ldx"] == 80
+
+
+@pytest.mark.parametrize("pitch", [1001, 1008, 1024])
+def test_one_row_of_odd_length_passes(T, pitch):
+    """Row strides have to be multiples of 16 bytes for the products; a single
+    row has none."""
+    x = OnGpu(torch.zeros(1, pitch, dtype=BF16)[:, :1001])
+    one = dict(begin=mat(1, dtype=torch.int64), count=mat(1, dtype=torch.int64))
+    product(T, x=x, w=OnGpu(torch.zeros(1, 32, 1008, dtype=BF16)[:, :, :1001]), out=mat(1, 32), **one)
+    product(T, x=mat(1, 64), w=mat(1, 1, 64), out=mat(1, 1), **one)
+    grad(T, dy=mat(1, 33), x=x, out=mat(1, 33, 1001), **one)
+    grad(T, dy=mat(1, 1), x=x, out=OnGpu(torch.zeros(1, 1, pitch, dtype=BF16)[:, :, :1001]), **one)
+    assert [c[2]["ldx"] for c in T.calls] == [1008, 64, 1008, 1008]
+    assert T.calls[1][2]["ldw"] == 64 and T.calls[1][2]["ldy"] == 8
+    assert T.calls[2][2]["lddy"] == 40 and T.calls[2][2]["lddw"] == 1001
+    assert T.calls[3][2]["lddy"] == 8 and T.calls[3][2]["lddw"] == 1008
+
+
+def test_matrices_of_one_row_lie_apart_as_their_stack_says(T):
+    w = OnGpu(torch.zeros(2, 5, 64, dtype=BF16)[:, :1])
+    product(T, w=w, out=mat(4, 1))
+    assert T.calls[0][2]["ldw"] == 320
+
+
+def test_one_row_in_place_keeps_one_stride(T):
+    row = OnGpu(torch.zeros(1, 1008, dtype=BF16)[:, :1001])
+    norm(T, x=row, weight=mat(1001), residual=row, out=row, total=None)
+    kw = T.calls[0][2]
+    assert kw["ldx"] == kw["ldr"] == kw["ldy"] == 1008
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pitch", [1001, 1008])
+def test_one_odd_row_on_the_gpu(pitch):
+    """Whole numbers: exact in any order.  The padding holds NaN."""
+    import __graft_entry__
+
+    __graft_entry__.build()
+    from collective_datapath_atom_gb300 import torch_api as A
+
+    def whole(*shape, cols):
+        t = torch.full(shape, float("nan"), device="cuda", dtype=BF16)
+        t[..., :cols] = torch.randint(-3, 4, (*shape[:-1], cols), device="cuda").bfloat16()
+        return t[..., :cols]
+
+    h = A.initialize(1, stream=torch.cuda.current_stream())
+    try:
+        k, n = 1001, 37
+        x, dy = whole(1, pitch, cols=k), whole(1, 40, cols=n)
+        w = whole(1, n, 1008, cols=k)
+        begin = torch.zeros(1, device="cuda", dtype=torch.int64)
+        count = torch.ones(1, device="cuda", dtype=torch.int64)
+        y = A.grouped_matmul(x, w, begin, count, h)
+        dx = A.grouped_matmul(dy, w, begin, count, h, transposed=True)
+        dw = A.grouped_matmul_weight_grad(dy, x, begin, count, h)
+        A.check(h)
+        assert torch.equal(y, (x.double() @ w[0].double().t()).float().bfloat16())
+        assert torch.equal(dx, (dy.double() @ w[0].double()).float().bfloat16())
+        assert torch.equal(dw[0], (dy.double().t() @ x.double()).float().bfloat16())
+        # rows of one element each, of a stack with a stride of its own
+        w1 = whole(2, 3, 1008, cols=k)[:, :1]
+        x2 = whole(2, 1008, cols=k)
+        y = A.grouped_matmul(x2, w1, torch.arange(2, device="cuda"), torch.ones(2, device="cuda").long(), h)
+        A.check(h)
+        want = (x2.double() * w1[:, 0].double()).sum(1, keepdim=True)
+        assert torch.equal(y, want.float().bfloat16())
+    finally:
+        A.finalize(h)
