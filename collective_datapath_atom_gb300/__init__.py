@@ -250,9 +250,10 @@ def _stream_handle(stream) -> int:
 class Context:
     """Owns one ``purlin_ctx*``; calls ``purlin_finalize`` on close."""
 
-    def __init__(self, handle: int, R: int):
+    def __init__(self, handle: int, R: int, stream_handle: int = 0):
         self.handle = ctypes.c_void_p(handle)
         self.R = R
+        self.stream_handle = stream_handle   # the cudaStream_t that calls launch on
 
     def close(self):
         if self.handle:
@@ -273,7 +274,7 @@ def purlin_init(R: int, stream=None) -> Context:
     h = ctypes.c_void_p(0)
     _ok(lib.purlin_init(int(R), ctypes.c_void_p(_stream_handle(stream)), ctypes.byref(h)),
         "purlin_init")
-    return Context(h.value, int(R))
+    return Context(h.value, int(R), _stream_handle(stream))
 
 
 def purlin_finalize(ctx: Context):
@@ -283,6 +284,7 @@ def purlin_finalize(ctx: Context):
 def purlin_set_stream(ctx: Context, stream):
     _ok(lib.purlin_set_stream(ctx.handle, ctypes.c_void_p(_stream_handle(stream))),
         "purlin_set_stream")
+    ctx.stream_handle = _stream_handle(stream)
 
 
 def _uniform(fn, name, ctx, src, dst, n, dtype, op, layout):

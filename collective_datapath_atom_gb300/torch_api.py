@@ -12,7 +12,10 @@ ctypes binding, so this module only marshals arguments.
     finalize(h)
 
 The layer operators that follow the collectives take one rank's tensors:
-``rms_norm``, ``grouped_matmul`` and their gradients.
+``rms_norm``, ``grouped_matmul`` and their gradients.  They run on the handle's
+stream (or on ``stream``), and so do the allocation and the zeroing of results
+that are not passed in.  Where that is not torch's current stream, order the two
+as for any stream's results: the inputs before the call, the results after it.
 """
 from __future__ import annotations
 
@@ -72,17 +75,13 @@ def _on(handle: Context, stream):
     waits for the previous stream, so it is skipped when nothing changes)."""
     if stream is None:
         return
-    h = _stream_handle(stream)
-    if h != getattr(handle, "stream_handle", None):
+    if _stream_handle(stream) != handle.stream_handle:
         purlin_set_stream(handle, stream)
-        handle.stream_handle = h
 
 
 def initialize(R: int, stream=None) -> Context:
     """A context for R rank buffers on the current CUDA device."""
-    handle = purlin_init(R, stream)
-    handle.stream_handle = _stream_handle(stream)
-    return handle
+    return purlin_init(R, stream)
 
 
 def finalize(handle: Context, stream=None):
@@ -178,6 +177,24 @@ def all_to_all_v(xs, outs, counts, handle, stream=None):
 
 # ------------------------------------------------------- layer operators ---
 
+def _new(handle, stream, device, shape, dtype, zero=False):
+    """A result for a call to write, of the stream that the call launches on.  Memory
+    of another stream may still be in use there, and a fill there could land after
+    the kernel."""
+    import torch
+
+    make = torch.zeros if zero else torch.empty
+    current = torch.cuda.current_stream(device)
+    h = handle.stream_handle if stream is None else _stream_handle(stream)
+    if h == current.cuda_stream:
+        return make(shape, device=device, dtype=dtype)
+    launch = torch.cuda.ExternalStream(h, device) if h else torch.cuda.default_stream(device)
+    with torch.cuda.stream(launch):
+        t = make(shape, device=device, dtype=dtype)
+    t.record_stream(current)   # the caller's: not to be reused while it reads
+    return t
+
+
 def _pitch(t, rows, stride):
     """Row stride to pass on for `rows` rows.  A single row's may be anything; it is
     rounded up to 16 bytes, which the products ask of a matrix's rows."""
@@ -229,12 +246,12 @@ def rms_norm(x, weight, handle, residual=None, out=None, total=None, scales=None
     ldt = _same_rows("total", total, x) if total is not None else 0
     kind = torch.float8_e4m3fn if quantize else x.dtype
     if out is None:
-        out = torch.empty(rows, hidden, device=x.device, dtype=kind)
+        out = _new(handle, stream, x.device, (rows, hidden), kind)
     if out.shape != x.shape:
         raise ValueError("out has the shape of x")
     ldy = _rows("out", out, (kind,))[2]
     if quantize and scales is None:
-        scales = torch.empty(rows, device=x.device)
+        scales = _new(handle, stream, x.device, (rows,), torch.float32)
     if scales is not None:
         if not quantize:
             raise ValueError("scales belong to a quantized output")
@@ -258,9 +275,10 @@ def rms_norm_backward(dy, total, weight, handle, dtotal=None, dx=None, dweight=N
     _vector("weight", weight, hidden, total.dtype)
     lddy = _same_rows("dy", dy, total)
     lddt = _same_rows("dtotal", dtotal, total) if dtotal is not None else 0
-    dx = torch.empty(rows, hidden, device=dy.device, dtype=dy.dtype) if dx is None else dx
+    dx = _new(handle, stream, dy.device, (rows, hidden), dy.dtype) if dx is None else dx
     lddx = _same_rows("dx", dx, total)
-    dweight = torch.empty(hidden, device=dy.device) if dweight is None else dweight
+    if dweight is None:
+        dweight = _new(handle, stream, dy.device, (hidden,), torch.float32)
     _vector("dweight", dweight, hidden, torch.float32)
     _on(handle, stream)
     purlin_rms_norm_backward(handle, dy, total, weight, dx, dweight, rows, hidden, eps, d,
@@ -305,7 +323,7 @@ def grouped_matmul(x, w, begin, count, handle, out=None, x_scales=None, w_scales
     rows, _, ldx = _rows("x", x, (w.dtype,), k)
     _groups(begin, count, groups)
     if out is None:
-        out = torch.zeros(rows, n, device=x.device, dtype=torch.bfloat16)
+        out = _new(handle, stream, x.device, (rows, n), torch.bfloat16, zero=True)
     out_rows, _, ldy = _rows("out", out, (torch.bfloat16,), n)
     if out_rows != rows:
         raise ValueError("out holds as many rows as x")
@@ -334,7 +352,7 @@ def grouped_matmul_weight_grad(dy, x, begin, count, handle, out=None, stream=Non
     groups = int(count.numel())
     _groups(begin, count, groups)
     if out is None:
-        out = torch.empty(groups, n, k, device=x.device, dtype=torch.bfloat16)
+        out = _new(handle, stream, x.device, (groups, n, k), torch.bfloat16)
     og, on, ok, lddw = _stack("out", out, (torch.bfloat16,))
     if (og, on, ok) != (groups, n, k):
         raise ValueError(f"out has shape {(og, on, ok)}, expected {(groups, n, k)}")
