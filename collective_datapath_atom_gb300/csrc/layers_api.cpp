@@ -51,7 +51,7 @@ Matrix group_array(const int64_t *p, int groups) {
 // The same elements in the same places: allowed where a thread reads an
 // element before it writes it.
 bool same(const Matrix &a, const Matrix &b) {
-    return a.p == b.p && a.pitch == b.pitch && a.width == b.width;
+    return a.p == b.p && a.pitch == b.pitch && a.width == b.width && a.rows == b.rows;
 }
 
 bool misaligned(const void *p, size_t to) {
@@ -171,10 +171,12 @@ purlin_status purlin_rms_norm(purlin_ctx *ctx, const void *x, size_t ldx, const 
     const Matrix my = matrix(y, rows, hidden, ldy, out_dtype);
     const Matrix mt = matrix(total, rows, hidden, ldt, dtype);
     const Matrix ms = matrix(scales, 1, rows, rows, PURLIN_F32);
-    for (const Matrix *o : {&my, &mt, &ms})
+    for (const Matrix *o : {&my, &mt})
         if (overlap(*o, mw) || (overlap(*o, mx) && !same(*o, mx)) ||
             (overlap(*o, mr) && !same(*o, mr)))
             return PURLIN_ERR_ALIAS;
+    // (scales are another row's elements, wherever in x they lie)
+    if (overlap(ms, mx) || overlap(ms, mr) || overlap(ms, mw)) return PURLIN_ERR_ALIAS;
     if (overlap(my, mt) || overlap(my, ms) || overlap(mt, ms)) return PURLIN_ERR_ALIAS;
     if (ctx == nullptr) return PURLIN_ERR_INVALID_ARG;
 
