@@ -608,9 +608,13 @@ purlin_status purlin_check(purlin_ctx *ctx) {
     if (cudaMemcpy(&word, ctx->err, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
         return PURLIN_ERR_CUDA;
     if (word == 0) return PURLIN_OK;
-    // a grouped product that gave up may have left its tiles' counters part-way
-    if (cudaMemset(ctx->err, 0, sizeof word) != cudaSuccess ||
-        cudaMemset(ctx->arrived, 0, kJoinCounters * sizeof(unsigned)) != cudaSuccess)
+    // a grouped product that gave up may have left its tiles' counters part-way.
+    // On the context's stream: a plain memset would be on the default stream, which a
+    // non-blocking one does not wait for, and could land in the next call.
+    if (cudaMemsetAsync(ctx->err, 0, sizeof word, ctx->stream) != cudaSuccess ||
+        cudaMemsetAsync(ctx->arrived, 0, kJoinCounters * sizeof(unsigned), ctx->stream) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(ctx->stream) != cudaSuccess)
         return PURLIN_ERR_CUDA;
     return static_cast<purlin_status>(word & 0xFF);
 }
