@@ -834,16 +834,17 @@ typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, 
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiled encode_tiled() {
-    static const EncodeTiled f = [] {
-        void *p = nullptr;
+    static std::atomic<void *> found{nullptr};   // not found: asked for again
+    void *p = found.load(std::memory_order_acquire);
+    if (p == nullptr) {
         cudaDriverEntryPointQueryResult r;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
                                              cudaEnableDefault, &r) != cudaSuccess ||
             r != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
+            return nullptr;
+        found.store(p, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(p);
 }
 
 // A tensor of rank 2 or 3 with rows `ld` elements apart, read in boxes of
@@ -865,8 +866,8 @@ bool make_map(CUtensorMap *m, const void *p, int dtype, int rank, size_t d0, siz
 
 template <int MODE, bool BF16, int CG>
 cudaError_t launch_tc(const GroupedArgs &a, const TcParams &p) {
-    static const cudaError_t ready = cudaFuncSetAttribute(
-        grouped_tc_kernel<MODE, BF16, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    static SharedMemoryLimit limit;
+    const cudaError_t ready = limit.raise(grouped_tc_kernel<MODE, BF16, CG>, (int)kSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(a.sms / CG * CG));

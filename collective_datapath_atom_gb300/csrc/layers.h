@@ -5,12 +5,34 @@
 
 #include <cuda_runtime_api.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 #include "../../include/purlin.h"
 
 namespace purlin {
+
+// Lets one kernel's dynamic shared memory grow, once on each device: the attribute
+// belongs to the device that is current, and a call that failed is made again.
+class SharedMemoryLimit {
+public:
+    template <typename K>
+    cudaError_t raise(K *kernel, int bytes) {
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = device < 64 ? 1ull << device : 0;   // past 64 devices: every time
+        if (raised_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) raised_.fetch_or(bit, std::memory_order_acq_rel);
+        return e;
+    }
+
+private:
+    std::atomic<uint64_t> raised_{0};
+};
 
 // ------------------------------------------------------------- RMS norm --
 

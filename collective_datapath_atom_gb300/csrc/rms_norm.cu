@@ -972,30 +972,28 @@ Shape staged_shape(size_t rows, size_t hidden, bool edge, int arrays, int sms, b
     return s;
 }
 
-// Lets a kernel's dynamic shared memory grow.
-template <typename K>
-cudaError_t prepared(K *kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
-}
+constexpr int kStagedSmem = 224 * 1024;   // most dynamic shared memory of a staged launch
 
 template <typename T, typename O, int V, bool EDGE>
 cudaError_t norm_typed(const NormArgs &a, NormParams &p) {
     if constexpr (V > 1) {
         const Shape s =
             staged_shape<V>(a.rows, a.hidden, EDGE, a.residual ? 2 : 1, a.sms, false);
-        auto run = [&](auto kernel) {
+        auto run = [&](auto kernel, SharedMemoryLimit &limit) {
+            const cudaError_t ready = limit.raise(kernel, kStagedSmem);
+            if (ready != cudaSuccess) return ready;
             kernel<<<s.grid, s.tx, s.smem, a.stream>>>(p);
             return cudaGetLastError();
         };
         p.stages = s.stages;
         if (s.items == 4) {
-            static const cudaError_t ready = prepared(norm_staged_kernel<T, O, V, 4, EDGE>);
-            return ready != cudaSuccess ? ready : run(norm_staged_kernel<T, O, V, 4, EDGE>);
+            static SharedMemoryLimit limit;
+            return run(norm_staged_kernel<T, O, V, 4, EDGE>, limit);
         }
         if constexpr (V == 4) {
             if (s.items == 8) {
-                static const cudaError_t ready = prepared(norm_staged_kernel<T, O, V, 8, EDGE>);
-                return ready != cudaSuccess ? ready : run(norm_staged_kernel<T, O, V, 8, EDGE>);
+                static SharedMemoryLimit limit;
+                return run(norm_staged_kernel<T, O, V, 8, EDGE>, limit);
             }
         }
     }
@@ -1080,7 +1078,9 @@ cudaError_t norm_backward_typed(const NormBackwardArgs &a, const NormBackwardPar
     }
     if constexpr (V > 1) {
         if (s.stages > 0) {
-            static const cudaError_t ready = prepared(norm_backward_staged_kernel<T, V, 4, EDGE>);
+            static SharedMemoryLimit limit;
+            const cudaError_t ready =
+                limit.raise(norm_backward_staged_kernel<T, V, 4, EDGE>, kStagedSmem);
             if (ready != cudaSuccess) return ready;
             norm_backward_staged_kernel<T, V, 4, EDGE><<<s.grid, s.tx, s.smem, a.stream>>>(p);
             return cudaGetLastError();
