@@ -277,19 +277,22 @@ purlin_status purlin_noalloc_check(purlin_stream stream);
  * the same inputs give the same bits.  Partial results go to a workspace the
  * context owns, grown by the first call that needs more: during graph capture
  * such a call returns UNSUPPORTED, so make it once before (the first call of a
- * kind also loads its kernel).  Launches overlap the end of the kernel before
+ * kind also loads its kernel).  Its calls share that memory: they, and replays
+ * of graphs that hold them, run one after another.  Launches overlap the end of the kernel before
  * them on the stream, and touch no memory until it is done.  rows, hidden, n
- * and k are at most 2^31 - 4096 (hidden: half that); offsets within a matrix may exceed 32 bits.  An
- * output may not overlap another buffer (ALIAS) except where stated. */
+ * and k are at most 2^31 - 4096 (hidden: half that); offsets within a matrix
+ * may exceed 32 bits.  An output may not overlap another buffer (ALIAS) except
+ * where stated. */
 
 /* Root-mean-square norm with the residual's addition, for each row:
  *   t = x + residual   (residual NULL: t = x)
  *   v = t / sqrt(mean(t^2) + eps) * weight
  * out_dtype == dtype: y = v, and scales must be NULL.  out_dtype E4M3:
  * scales[row] = max(max |v| / 448, 2^-126) and y = v / scales[row], a binary32
- * quotient, in e4m3 (nearest even; the maximum skips NaN, and a NaN element is e4m3 NaN).  An
- * all-zero row gives zeros.  total (or NULL) receives t: the residual stream
- * of the next layer.  The norm is of the unrounded t.
+ * quotient, in e4m3 (nearest even; the maximum skips NaN, and a NaN element is
+ * e4m3 NaN).  An all-zero row gives zeros where eps > 0, and NaN (0 / 0) where
+ * it is 0.  total (or NULL) receives t: the residual stream of the next layer.
+ * The norm is of the unrounded t.
  * dtype F32 or BF16, that of x, residual, weight and total.  Pointers need
  * only their type's alignment; rows on 16-byte boundaries take 128-bit
  * accesses.  total may be x or residual, and y may be x or residual when the

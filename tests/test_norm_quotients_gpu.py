@@ -132,6 +132,22 @@ def test_tiny_and_infinite_scales(P, ctx, rows, hidden):
     assert bool(got[:, 0].isnan().all()) and bool((got[:, 1:] == 0).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,hidden", [(3, 264), (3, 1021), (900, 2048), (2, 40000)])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-5])
+def test_zero_rows(P, ctx, rows, hidden, eps):
+    """0 / root(0 + eps): zeros, or NaN without an eps, as the formula has it."""
+    x, w = torch.zeros(rows, hidden, device="cuda"), torch.ones(hidden, device="cuda")
+    y, scales = torch.empty_like(x), torch.empty(rows, device="cuda")
+    q = torch.empty(rows, hidden, device="cuda", dtype=torch.float8_e4m3fn)
+    P.purlin_rms_norm(ctx, x, w, y, rows, hidden, eps, 0)
+    P.purlin_rms_norm(ctx, x, w, q, rows, hidden, eps, 0, P.PURLIN_E4M3, scales=scales)
+    P.purlin_check(ctx)
+    for t in (y, q.float()):
+        assert bool((t.isnan() if eps == 0 else t == 0).all())
+    assert bool((scales == 2.0 ** -126).all())
+
+
 # hidden sizes whose binary32 reciprocal is not exact; few rows and many
 @pytest.mark.gpu
 @pytest.mark.parametrize("hidden", [1100, 1101, 2052, 4099, 7168])
