@@ -26,11 +26,11 @@
 // Sums are binary32 in tensor memory, rounded once to bf16 on the way out.
 //
 // Bound by the tensor cores at prefill sizes: 16384 x 7168 x 2048 bf16 in one
-// group takes 276 us (1.74 PFLOP/s, the card at its power limit; one cuBLAS product
-// 285), over 8 Zipf groups 280 us in a short burst and 316 in a long one, the
-// tensor pipe 79% active; e4m3 at twice the channels 272 and 319 (3.5 and 3.0
-// PFLOP/s); data gradient 260, weight gradient 294 us.  Bound by the weights' bytes
-// at decode sizes: 8 rows on 5 of 8 experts, 147 MB, 31 us; 128 rows on 64
+// group takes 246 us in a short burst and 278 in long runs at the card's power limit
+// (1.73 PFLOP/s; one cuBLAS product 288 there), over 8 Zipf groups 282 and 316, the
+// tensor pipe 80% active; e4m3 at twice the channels 275 and 317 (3.5 and 3.0
+// PFLOP/s); data gradient 260, weight gradient 297 us alone.  Bound by the weights'
+// bytes at decode sizes: 8 rows on 5 of 8 experts, 147 MB, 31 us; 128 rows on 64
 // experts, e4m3, 269 MB, 47 us (5.7 TB/s), of which about 5 us are the launch, the
 // plan, the first load's latency and the join.
 #include <cuda_bf16.h>
@@ -168,8 +168,8 @@ __device__ __forceinline__ bool group_bad(long long b, long long c, long long ro
 // plan already (`bad`: one of them lies outside the rows).  Groups that hold more
 // rows than there are overlap, and are refused too; a plan of bad groups has no
 // tiles.  This stands before the first load of every CTA, so it is one warp's
-// work with one block barrier behind it, and sums by redux (3100 clocks by block
-// and shared atomics, 5.3 us of a whole small product).
+// work with one block barrier behind it, and sums by redux: by the block, with
+// shared atomics, it took several times as long.
 template <int MODE, int BK, int CG>
 __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool bad) {
     const int lane = threadIdx.x;
@@ -265,8 +265,8 @@ __device__ void lay_out(Plan &t, const TcParams &p, int i_tiles, int ctas, bool 
     t.width = width;
     // Fewer tiles than CTAs: runs of K blocks, where the time that idle CTAs would
     // waste is more than a join's.  (More tiles go round whole: CTAs in step share
-    // what they read of the weights, and with the last wave cut into runs
-    // 2048 x 7168 x 2048 took 99 us instead of 65.)
+    // what they read of the weights; with the last wave cut into runs they
+    // read them twice, and products of a few waves took half as long again.)
     const long long idle = ctas - tiles;
     const bool cut = tiles > 0 && idle > 0 &&
                      idle * spent >= (long long)kJoinBlocks * ctas * block_cost(width) * tiles;
@@ -887,11 +887,16 @@ cudaError_t launch_tc(const GroupedArgs &a, const TcParams &p) {
 template <int MODE, bool BF16>
 cudaError_t launch_mode(const GroupedArgs &a, const TcParams &p) {
     // A pair halves what each CTA loads of B, and its tiles are twice as wide: it
-    // pays once there is work for it.  Single CTAs against pairs, us: 1024 rows in one
-    // group, 2048 x 2048, 13.2 and 14.0; 2048 rows in 8 groups, 1024 x 2048, 16.4 and
-    // 16.4, 7168 x 2048 69.1 and 64.3; 16384 rows in 64 groups, 2048 x 2048, 146 and 121;
-    // 16384 rows in 8, 7168 x 2048, 322 and 285.  Channels that fill a wider tile badly
+    // pays once there is work for it.  Single CTAs against pairs, us, of equal groups:
+    // 1024 rows in one, 2048 x 2048, 12.6 and 13.6; 2048 rows in 8, 1024 x 2048, 14.6
+    // and 15.2, 7168 x 2048 54.8 and 51.6; 16384 rows in 64, 2048 x 2048, 123 and 114;
+    // 16384 rows in 8, 2048 x 7168, 321 and 290.  Channels that fill a wider tile badly
     // stay with single CTAs (384: a third of it empty).
+    // The counts are on the device: `rows` is what the buffer holds, an upper bound.  In
+    // buffers of full capacity with few rows in them pairs lose a little: 128 rows on 64
+    // experts of 1024 places, e4m3 1024 x 4096, 47.7 and 48.5, bf16 1024 x 2048 47.5 and
+    // 48.2; 256 rows on 8 of 2048, 2048 x 7168, 41.9 and 42.5 (2000 rows 68.4 and 65.3);
+    // 20 rows on 8 of 1024, 1024 x 1024, 7.3 and 8.2.
     const double work = (double)a.rows * (double)a.n * (double)a.k;
     const size_t wide = ((size_t)p.ni + 255) / 256 * 2, narrow = ((size_t)p.ni + 127) / 128;
     const bool pair = work >= 8e9 && 8 * wide <= 9 * narrow && a.sms >= 2;

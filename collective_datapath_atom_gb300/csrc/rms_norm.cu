@@ -22,7 +22,9 @@
 // written in 16-byte windows all the same: a window starts `phase` elements
 // before the row, and only the row's first and last windows go element by
 // element.  The grid is a multiple of the windows' elements, so all of a
-// block's rows have one phase and a thread's columns stay the same.
+// block's rows have one phase and a thread's columns stay the same.  Operands at
+// different phases go element by element (16384 x 7168 bf16 331 us instead of 158,
+// backward 494 instead of 119).
 //
 // Both are bound by bytes.  16384 x 7168 bf16 with a residual to e4m3: 124 us, 6.6
 // TB/s (99% of a copy's rate); backward of 32768 x 4096 bf16: 171 us, 6.3 TB/s.  A
@@ -244,8 +246,8 @@ __device__ __forceinline__ Window<T, V> read_weight(const T *w, int e, int hidde
 constexpr int norm_threads(int held) { return held <= 8 ? 1024 : 512; }
 constexpr int kBackwardThreads = 512, kStagedThreads = 512;
 constexpr int kShortRows = 8;   // rows of a block with a warp a row
-// Backward, fewer rows a block and fewer blocks: less to join (4000 x 768 bf16 16.6
-// us, with 8 rows and 1024 threads an SM 32.1; 32768 x 512 31.1 and 39.2).
+// Backward, fewer rows a block and fewer blocks: less to join (4000 x 768 bf16 16.4
+// us, with 8 rows and 1024 threads an SM 31.6; 32768 x 512 30.7 and 39.0).
 constexpr int kBackwardShortRows = 4, kBackwardThreadsSm = 512;
 
 // A thread holds ITEMS windows of V elements of its row.  blockDim.y rows a
@@ -541,7 +543,10 @@ norm_staged_kernel(const __grid_constant__ NormParams p) {
 }
 
 // Rows too long for the registers: x and the residual are read again (from
-// the L2 cache mostly) for the output, and a third time for an e4m3 output.
+// the L2 cache mostly) for the output, and a third time for an e4m3 output.  More
+// than 16384 elements, or 16384 with an edge in bf16, which is one window more than
+// the threads hold: 4096 x 16384 bf16 with a weight off its boundary takes 233 us,
+// aligned 92 (to e4m3 294 and 78, backward 258 and 86).
 template <typename T, typename O>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormParams p) {
     __shared__ float sums[32], maxes[32];
@@ -591,8 +596,9 @@ struct NormBackwardParams {
 
 // blockDim.y rows a block, more than one only where blockDim.x is one warp: then
 // the warps' shares of dweight are added up in shared memory, warp by warp.  WIDE:
-// blocks of up to 1024 threads, with registers for a row and dweight's sums but not
-// for the weight, which every row reads again.
+// blocks of up to 1024 threads, whose 64 registers do not hold a row, its gradient
+// and dweight's sums: 300 bytes a thread are spilled, and the weight is read again
+// every row.  Still faster than the long kernel (`wide`, in backward_shape).
 template <typename T, int V, int ITEMS, bool EDGE, bool WIDE = false>
 __global__ void __launch_bounds__(WIDE ? 1024 : kBackwardThreads)
 norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
@@ -935,8 +941,9 @@ Shape register_shape(size_t rows, size_t hidden, bool edge, int most_items, int 
 // a warp, or the stages do not fit.  About 14 warps an SM and 96 KiB of
 // rows on their way keep the memory busy; with twice that many the reads run so
 // far ahead of the writes that it slows down (e4m3 from 7168 bf16 columns with a
-// residual: two blocks of two stages 6.15 TB/s, three 5.48, one of four 4.38).
-// `late`: a stage is refilled only a row later, so two of them leave gaps.
+// residual: two blocks of two stages 6.63 TB/s, of four 3.70; three of two 5.56, one
+// of four 4.26).  `late`: a stage is refilled only a row later, so two of them leave
+// gaps (32768 x 4096 bf16: three 170 us, two 198).
 template <int V>
 Shape staged_shape(size_t rows, size_t hidden, bool edge, int arrays, int sms, bool late) {
     Shape s;
@@ -946,7 +953,7 @@ Shape staged_shape(size_t rows, size_t hidden, bool edge, int arrays, int sms, b
     const size_t windows = windows_of<V>(hidden, edge);
     const size_t stage = (hidden + 2 * (V - 1)) / V * 16 * (size_t)arrays;   // as RowRing has it
     // a row that fits a warp's registers stays there; backward, where dweight's sums
-    // need them, less of one does (32768 x 1024 bf16 55.7 us, from registers 60.8)
+    // need them, less of one does (32768 x 1024 bf16 55.4 us, from registers 61.5)
     if (V == 1 || windows <= (late ? 100 : 128)) return s;
     const int items = warps_of(windows, 4) <= (unsigned)kStagedThreads ? 4 : 8;
     const unsigned tx = warps_of(windows, items);
@@ -959,8 +966,8 @@ Shape staged_shape(size_t rows, size_t hidden, bool edge, int arrays, int sms, b
         if (fit < least) continue;
         const size_t stages =
             std::max(late ? std::min<size_t>(fit, 3) : least, std::min(fit, kFlight / (b * stage)));
-        // forward, from a row an SM on (500 x 7168 to e4m3 8.3 us, from registers 12.3);
-        // backward, where a block has two (509 x 1021 f32 10.4 us, from registers 8.4)
+        // forward, from a row an SM on (500 x 7168 to e4m3 8.2 us, from registers 12.3);
+        // backward, where a block has two (509 x 1021 f32 10.3 us, from registers 7.5)
         if (rows < (late ? 2 * b : 1) * (size_t)sms) return s;
         s.items = items;
         s.tx = tx;
@@ -1055,8 +1062,8 @@ BackwardShape backward_shape(const NormBackwardArgs &a) {
                                        kBackwardThreadsSm, threads);
     const unsigned most = s.windows ? warps_of(windows_of<V>(a.hidden, s.edge), 4) : 2048;
     if (s.items == 0 && V == 4 && most <= 1024) {
-        // rows of 8192 to 16384 f32: a block an SM (3000 x 16384 186 us, read again from
-        // the L2 cache 312)
+        // rows of 8192 to 16384 f32: a block an SM (3000 x 16384 140 us, read again from
+        // the L2 cache 263; with dtotal 184 and 313; 3000 x 8200 98 and 121)
         s.wide = true;
         s.items = 4;
         s.tx = most;
@@ -1106,7 +1113,7 @@ cudaError_t norm_backward_any(const NormBackwardArgs &a) {
                           : s.edge   ? norm_backward_typed<T, V, true>(a, p, s)
                                      : norm_backward_typed<T, V, false>(a, p, s);
     if (e != cudaSuccess) return e;
-    // the join's launch overlaps the rows' kernel (3 us less at 509 x 1021 f32)
+    // the join's launch overlaps the rows' kernel (509 x 1021 f32 7.5 us, launched after it 9.1)
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)((a.hidden + 31) / 32));
     c.blockDim = dim3(32, kJoinRows);
