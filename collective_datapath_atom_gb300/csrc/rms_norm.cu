@@ -154,17 +154,6 @@ __device__ __forceinline__ float reduce_row(float v, bool warp_only, float *shar
     return v;
 }
 
-struct NormParams {
-    const void *x, *residual, *weight;
-    void *y, *total;
-    float *scales;
-    size_t ldx, ldr, ldy, ldt, rows;
-    uint32_t hidden, phase;   // phase of row 0's first element in its window
-    float eps;
-    int stages;               // of a staged launch
-    unsigned long long *err;
-};
-
 // Elements between a window's start and the row's, for the row at `row`.
 template <int V>
 __device__ __forceinline__ int phase_of(uint32_t phase, size_t ld, size_t row) {
@@ -240,96 +229,6 @@ __device__ __forceinline__ Window<T, V> read_weight(const T *w, int e, int hidde
     for (int j = 0; j < V; ++j)
         if (e + j >= 0 && e + j < hidden) k.set(j, bits_of(w + e + j));
     return k;
-}
-
-// Threads of a block: 1024 where a thread holds little, else the registers for it.
-constexpr int norm_threads(int held) { return held <= 8 ? 1024 : 512; }
-constexpr int kBackwardThreads = 512, kStagedThreads = 512;
-constexpr int kShortRows = 8;   // rows of a block with a warp a row
-// Backward, fewer rows a block and fewer blocks: less to join (4000 x 768 bf16 16.4
-// us, with 8 rows and 1024 threads an SM 31.6; 32768 x 512 30.7 and 39.0).
-constexpr int kBackwardShortRows = 4, kBackwardThreadsSm = 512;
-
-// A thread holds ITEMS windows of V elements of its row.  blockDim.y rows a
-// block; more than one only where blockDim.x is one warp.  Up to 64 bytes a
-// thread the next row and the weight are kept in registers too.
-template <typename T, typename O, int V, int ITEMS, bool EDGE>
-__global__ void __launch_bounds__(norm_threads(ITEMS * V))
-norm_kernel(const __grid_constant__ NormParams p) {
-    constexpr bool AHEAD = ITEMS * V * sizeof(T) <= 64;
-    __shared__ float sums[2][32], maxes[2][32];   // rows take turns: a barrier a sum
-    const bool warp_only = blockDim.x == 32;
-    const size_t step = (size_t)gridDim.x * blockDim.y;
-    size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (row >= p.rows) return;   // whole warps; blockDim.y > 1 has no block barrier
-    const int hidden = (int)p.hidden, phase = EDGE ? phase_of<V>(p.phase, p.ldx, row) : 0;
-    const int e0 = (int)threadIdx.x * V - phase, estep = (int)blockDim.x * V;
-    const T *w = static_cast<const T *>(p.weight);
-    Window<T, V> wk[ITEMS], xk[ITEMS], rk[ITEMS];
-    auto fetch = [&](size_t at) {
-        const T *x = static_cast<const T *>(p.x) + at * p.ldx;
-        const T *res = static_cast<const T *>(p.residual) + at * p.ldr;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) xk[i] = read_window<T, V, EDGE>(x, e0 + i * estep, hidden);
-        if (p.residual) {
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) rk[i] = read_window<T, V, EDGE>(res, e0 + i * estep, hidden);
-        }
-    };
-    fetch(row);
-    if constexpr (AHEAD) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) wk[i] = read_weight<T, V, EDGE>(w, e0 + i * estep, hidden);
-    }
-    for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
-        float t[ITEMS][V];
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                t[i][j] = xk[i].at(j);
-                if (p.residual) t[i][j] += rk[i].at(j);
-                ss = fmaf(t[i][j], t[i][j], ss);
-            }
-        if constexpr (AHEAD) {
-            if (row + step < p.rows) fetch(row + step);
-        } else {
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) wk[i] = read_weight<T, V, EDGE>(w, e0 + i * estep, hidden);
-        }
-        if (p.total) {
-            T *total = static_cast<T *>(p.total) + row * p.ldt;
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) write_window<T, V, EDGE>(total, e0 + i * estep, hidden, t[i]);
-        }
-        const float r = rsqrtf(reduce_row<Sum>(ss, warp_only, sums[turn]) / (float)p.hidden + p.eps);
-        O *y = static_cast<O *>(p.y) + row * p.ldy;
-        float most = 0.f;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                // a window's elements outside the row are zero and stay out of the
-                // maximum, unless r is infinite
-                t[i][j] = t[i][j] * r * wk[i].at(j);
-                most = fmaxf(most, fabsf(t[i][j]));
-            }
-            if constexpr (sizeof(O) != 1) write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
-        }
-        if constexpr (sizeof(O) == 1) {
-            // fmaxf passes over NaN: the scale stays a number, the elements are NaN
-            const float scale =
-                fmaxf(reduce_row<Max>(most, warp_only, maxes[turn]) / kE4m3Max, kScaleMin);
-            divide_row(t, scale);
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
-            if (threadIdx.x == 0) p.scales[row] = scale;
-        }
-        if constexpr (!AHEAD) {
-            if (row + step < p.rows) fetch(row + step);
-        }
-    }
 }
 
 // ------------------------------------------------------------ staged rows --
@@ -464,6 +363,144 @@ struct WeightStage {
         return k;
     }
 };
+
+// Whether windows of V elements fit rows at p the way they fit rows at q: the
+// same place within a window, row after row.
+template <int V>
+bool in_step(const void *p, size_t ldp, size_t esp, const void *q, size_t ldq, size_t esq) {
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) / esp % V ==
+                                reinterpret_cast<uintptr_t>(q) / esq % V &&
+                            ldp % V == ldq % V);
+}
+
+// How a launch covers its rows.
+struct Shape {
+    int items = 0;    // windows a thread; 0: the row does not fit the registers
+    unsigned tx = 0, ty = 1, grid = 0;
+    int stages = 0;   // of a staged launch, else 0
+    size_t smem = 0;
+};
+
+// Windows of a row; with edges, at the worst phase.
+template <int V>
+size_t windows_of(size_t hidden, bool edge) {
+    return edge ? (hidden + 2 * (V - 1)) / V : hidden / V;
+}
+
+unsigned warps_of(size_t windows, int items) {
+    return (unsigned)((windows + items - 1) / items + 31) / 32 * 32;
+}
+
+}  // namespace
+}  // namespace purlin
+
+// What stands above, a row's windows, sums and ring, serves block_norm.cu too, which
+// includes this file for it.
+#ifndef PURLIN_ROWS_ONLY
+
+namespace purlin {
+namespace {
+
+struct NormParams {
+    const void *x, *residual, *weight;
+    void *y, *total;
+    float *scales;
+    size_t ldx, ldr, ldy, ldt, rows;
+    uint32_t hidden, phase;   // phase of row 0's first element in its window
+    float eps;
+    int stages;               // of a staged launch
+    unsigned long long *err;
+};
+
+// Threads of a block: 1024 where a thread holds little, else the registers for it.
+constexpr int norm_threads(int held) { return held <= 8 ? 1024 : 512; }
+constexpr int kBackwardThreads = 512, kStagedThreads = 512;
+constexpr int kShortRows = 8;   // rows of a block with a warp a row
+// Backward, fewer rows a block and fewer blocks: less to join (4000 x 768 bf16 16.4
+// us, with 8 rows and 1024 threads an SM 31.6; 32768 x 512 30.7 and 39.0).
+constexpr int kBackwardShortRows = 4, kBackwardThreadsSm = 512;
+
+// A thread holds ITEMS windows of V elements of its row.  blockDim.y rows a
+// block; more than one only where blockDim.x is one warp.  Up to 64 bytes a
+// thread the next row and the weight are kept in registers too.
+template <typename T, typename O, int V, int ITEMS, bool EDGE>
+__global__ void __launch_bounds__(norm_threads(ITEMS * V))
+norm_kernel(const __grid_constant__ NormParams p) {
+    constexpr bool AHEAD = ITEMS * V * sizeof(T) <= 64;
+    __shared__ float sums[2][32], maxes[2][32];   // rows take turns: a barrier a sum
+    const bool warp_only = blockDim.x == 32;
+    const size_t step = (size_t)gridDim.x * blockDim.y;
+    size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (row >= p.rows) return;   // whole warps; blockDim.y > 1 has no block barrier
+    const int hidden = (int)p.hidden, phase = EDGE ? phase_of<V>(p.phase, p.ldx, row) : 0;
+    const int e0 = (int)threadIdx.x * V - phase, estep = (int)blockDim.x * V;
+    const T *w = static_cast<const T *>(p.weight);
+    Window<T, V> wk[ITEMS], xk[ITEMS], rk[ITEMS];
+    auto fetch = [&](size_t at) {
+        const T *x = static_cast<const T *>(p.x) + at * p.ldx;
+        const T *res = static_cast<const T *>(p.residual) + at * p.ldr;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) xk[i] = read_window<T, V, EDGE>(x, e0 + i * estep, hidden);
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) rk[i] = read_window<T, V, EDGE>(res, e0 + i * estep, hidden);
+        }
+    };
+    fetch(row);
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) wk[i] = read_weight<T, V, EDGE>(w, e0 + i * estep, hidden);
+    }
+    for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+        float t[ITEMS][V];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                t[i][j] = xk[i].at(j);
+                if (p.residual) t[i][j] += rk[i].at(j);
+                ss = fmaf(t[i][j], t[i][j], ss);
+            }
+        if constexpr (AHEAD) {
+            if (row + step < p.rows) fetch(row + step);
+        } else {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) wk[i] = read_weight<T, V, EDGE>(w, e0 + i * estep, hidden);
+        }
+        if (p.total) {
+            T *total = static_cast<T *>(p.total) + row * p.ldt;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) write_window<T, V, EDGE>(total, e0 + i * estep, hidden, t[i]);
+        }
+        const float r = rsqrtf(reduce_row<Sum>(ss, warp_only, sums[turn]) / (float)p.hidden + p.eps);
+        O *y = static_cast<O *>(p.y) + row * p.ldy;
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                // a window's elements outside the row are zero and stay out of the
+                // maximum, unless r is infinite
+                t[i][j] = t[i][j] * r * wk[i].at(j);
+                most = fmaxf(most, fabsf(t[i][j]));
+            }
+            if constexpr (sizeof(O) != 1) write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
+        }
+        if constexpr (sizeof(O) == 1) {
+            // fmaxf passes over NaN: the scale stays a number, the elements are NaN
+            const float scale =
+                fmaxf(reduce_row<Max>(most, warp_only, maxes[turn]) / kE4m3Max, kScaleMin);
+            divide_row(t, scale);
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) write_window<O, V, EDGE>(y, e0 + i * estep, hidden, t[i]);
+            if (threadIdx.x == 0) p.scales[row] = scale;
+        }
+        if constexpr (!AHEAD) {
+            if (row + step < p.rows) fetch(row + step);
+        }
+    }
+}
 
 template <typename T, typename O, int V, int ITEMS, bool EDGE>
 __global__ void __launch_bounds__(kStagedThreads, 2)
@@ -883,33 +920,6 @@ norm_join_kernel(const float *partial, float *dweight, uint32_t hidden, int part
     dweight[e] = v;
 }
 
-// Whether windows of V elements fit rows at p the way they fit rows at q: the
-// same place within a window, row after row.
-template <int V>
-bool in_step(const void *p, size_t ldp, size_t esp, const void *q, size_t ldq, size_t esq) {
-    return p == nullptr || (reinterpret_cast<uintptr_t>(p) / esp % V ==
-                                reinterpret_cast<uintptr_t>(q) / esq % V &&
-                            ldp % V == ldq % V);
-}
-
-// How a launch covers its rows.
-struct Shape {
-    int items = 0;    // windows a thread; 0: the row does not fit the registers
-    unsigned tx = 0, ty = 1, grid = 0;
-    int stages = 0;   // of a staged launch, else 0
-    size_t smem = 0;
-};
-
-// Windows of a row; with edges, at the worst phase.
-template <int V>
-size_t windows_of(size_t hidden, bool edge) {
-    return edge ? (hidden + 2 * (V - 1)) / V : hidden / V;
-}
-
-unsigned warps_of(size_t windows, int items) {
-    return (unsigned)((windows + items - 1) / items + 31) / 32 * 32;
-}
-
 // Rows on the registers alone: the fewest windows a thread that `threads(items)`
 // threads allow, which is the quickest for a block's first row.
 template <int V, typename F>
@@ -1149,3 +1159,5 @@ cudaError_t launch_norm_backward(const NormBackwardArgs &a) {
 }
 
 }  // namespace purlin
+
+#endif  // PURLIN_ROWS_ONLY
