@@ -23,6 +23,8 @@ PURLIN_F32, PURLIN_BF16, PURLIN_E4M3 = 0, 1, 2
 PURLIN_COPY, PURLIN_SUM = 0, 1
 PURLIN_PACKED, PURLIN_SCATTERED, PURLIN_TRANSPOSED = 0, 1, 2
 PURLIN_WEIGHTS_NK, PURLIN_WEIGHTS_KN = 0, 1
+PURLIN_GATE_COLUMNS, PURLIN_GATE_ROWS = 0, 1
+PURLIN_SOFTMAX, PURLIN_SIGMOID = 0, 1
 
 PURLIN_OK = 0
 PURLIN_ERR_INVALID_ARG = 1
@@ -101,6 +103,15 @@ class purlin_device_coll(ctypes.Structure):
                 ("owner", ctypes.c_void_p)]
 
 
+class purlin_router(ctypes.Structure):
+    """How tokens are routed to experts (include/purlin.h).  Fields left out are
+    0: one group, its value the largest choice, a scale of 1."""
+    _fields_ = [("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("scores", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class purlin_packet_channel(ctypes.Structure):
     """A payload+flag packet channel between CTAs of one launch (include/purlin.h)."""
     _fields_ = [("staging", ctypes.c_void_p), ("state", ctypes.c_void_p),
@@ -162,6 +173,26 @@ _SIGNATURES = {
         ctypes.c_int, ctypes.c_int]),
     "purlin_grouped_matmul_weight_grad": (ctypes.c_int, [
         _CTX, _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _VP, ctypes.c_int, _SZ, _SZ, _SZ,
+        ctypes.c_int]),
+    "purlin_block_norm": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _VP, _SZ, ctypes.c_int, ctypes.c_float, _VP, _SZ, ctypes.c_float, _VP,
+        _VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, ctypes.c_float, ctypes.c_int, ctypes.c_int]),
+    "purlin_block_norm_backward": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, ctypes.c_int, ctypes.c_float,
+        ctypes.c_float, _VP, _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ, _SZ, ctypes.c_float,
+        ctypes.c_int]),
+    "purlin_route": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _VP, _VP, _SZ, ctypes.POINTER(purlin_router), ctypes.c_int]),
+    "purlin_route_backward": (ctypes.c_int, [
+        _CTX, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ, ctypes.POINTER(purlin_router), ctypes.c_int]),
+    "purlin_expert_order": (ctypes.c_int, [
+        _CTX, _VP, _VP, _VP, _VP, _SZ, ctypes.c_int, _SZ]),
+    "purlin_dispatch_rows": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ, ctypes.c_int, _SZ, _SZ, ctypes.c_int]),
+    "purlin_combine_rows": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ, _SZ, ctypes.c_int, _SZ, _SZ, ctypes.c_int]),
+    "purlin_combine_rows_backward": (ctypes.c_int, [
+        _CTX, _VP, _SZ, _VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ, ctypes.c_int, _SZ, _SZ,
         ctypes.c_int]),
     "purlin_empty_launch": (ctypes.c_int, [ctypes.c_void_p]),
     "purlin_touch_launch": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
@@ -431,6 +462,94 @@ def purlin_grouped_matmul_weight_grad(ctx, dy, x, dw, begin, count, groups, rows
                                                groups, rows, n, k, dtype)
     if st:
         _ok(st, "purlin_grouped_matmul_weight_grad")
+
+
+def purlin_block_norm(ctx, x, weight, y, rows, hidden, eps, dtype, out_dtype=None, residual=None,
+                      post_weight=None, gate=None, gate_layout=PURLIN_GATE_COLUMNS,
+                      residual_scale=1.0, block_scale=1.0, total=None, scales=None, ldx=0, ldg=0,
+                      ldr=0, ldy=0, ldt=0):
+    """Norms after and before a block, with its gate and the residual's addition
+    between them; ``out_dtype`` PURLIN_E4M3 writes ``scales``.  ``weight`` and
+    ``y`` None: only ``total``."""
+    st = lib.purlin_block_norm(ctx.handle, _addr(x), ldx, _addr(post_weight), _addr(gate), ldg,
+                               gate_layout, block_scale, _addr(residual), ldr, residual_scale,
+                               _addr(weight), _addr(y), ldy, _addr(total), ldt, _addr(scales),
+                               rows, hidden, eps, dtype, dtype if out_dtype is None else out_dtype)
+    if st:
+        _ok(st, "purlin_block_norm")
+
+
+def purlin_block_norm_backward(ctx, dy, x, total, weight, dx, dweight, rows, hidden, eps, dtype,
+                               dtotal=None, post_weight=None, gate=None,
+                               gate_layout=PURLIN_GATE_COLUMNS, residual_scale=1.0,
+                               block_scale=1.0, dresidual=None, dpost_weight=None, dgate=None,
+                               lddy=0, lddt=0, ldx=0, ldt=0, ldg=0, lddx=0, lddr=0, lddg=0):
+    """Gradients of :func:`purlin_block_norm` at ``x`` and ``total``; ``dweight``,
+    ``dpost_weight`` and a column gate's ``dgate`` are float32."""
+    st = lib.purlin_block_norm_backward(
+        ctx.handle, _addr(dy), lddy, _addr(dtotal), lddt, _addr(x), ldx, _addr(total), ldt,
+        _addr(post_weight), _addr(gate), ldg, gate_layout, block_scale, residual_scale,
+        _addr(weight), _addr(dx), lddx, _addr(dresidual), lddr, _addr(dpost_weight), _addr(dgate),
+        lddg, _addr(dweight), rows, hidden, eps, dtype)
+    if st:
+        _ok(st, "purlin_block_norm_backward")
+
+
+def purlin_route(ctx, logits, weights, chosen, tokens, router, dtype, bias=None, ld=0):
+    """Each token's ``top_k`` experts (int32, falling) and their weights (float32)
+    from its logits; ``router`` is a :class:`purlin_router`."""
+    st = lib.purlin_route(ctx.handle, _addr(logits), ld, _addr(bias), _addr(weights),
+                          _addr(chosen), tokens, ctypes.byref(router), dtype)
+    if st:
+        _ok(st, "purlin_route")
+
+
+def purlin_route_backward(ctx, dweights, logits, chosen, dlogits, tokens, router, dtype, ld=0,
+                          ldd=0):
+    """Gradient of :func:`purlin_route`'s weights with respect to the logits."""
+    st = lib.purlin_route_backward(ctx.handle, _addr(dweights), _addr(logits), ld, _addr(chosen),
+                                   _addr(dlogits), ldd, tokens, ctypes.byref(router), dtype)
+    if st:
+        _ok(st, "purlin_route_backward")
+
+
+def purlin_expert_order(ctx, chosen, place, begin, count, slots, groups, capacity=0):
+    """The row of each slot in the order of the experts, packed or in buffers of
+    ``capacity`` rows (-1 past it), and the experts' first rows and counts (int64)."""
+    st = lib.purlin_expert_order(ctx.handle, _addr(chosen), _addr(place), _addr(begin),
+                                 _addr(count), slots, groups, capacity)
+    if st:
+        _ok(st, "purlin_expert_order")
+
+
+def purlin_dispatch_rows(ctx, x, place, out, tokens, top_k, cols, out_rows, dtype, scales=None,
+                         out_scales=None, ldx=0, ldo=0):
+    """A copy of each token's row (and scale) at each of its places."""
+    st = lib.purlin_dispatch_rows(ctx.handle, _addr(x), ldx, _addr(scales), _addr(place),
+                                  _addr(out), ldo, _addr(out_scales), tokens, top_k, cols,
+                                  out_rows, dtype)
+    if st:
+        _ok(st, "purlin_dispatch_rows")
+
+
+def purlin_combine_rows(ctx, rows, place, y, tokens, top_k, cols, n_rows, dtype, weights=None,
+                        shared=None, ldr=0, lds=0, ldy=0):
+    """The weighted sum of the rows at a token's places, on ``shared`` if given."""
+    st = lib.purlin_combine_rows(ctx.handle, _addr(rows), ldr, _addr(weights), _addr(place),
+                                 _addr(shared), lds, _addr(y), ldy, tokens, top_k, cols, n_rows,
+                                 dtype)
+    if st:
+        _ok(st, "purlin_combine_rows")
+
+
+def purlin_combine_rows_backward(ctx, dy, rows, place, weights, drows, dweights, tokens, top_k,
+                                 cols, n_rows, dtype, lddy=0, ldr=0, lddr=0):
+    """Gradients of :func:`purlin_combine_rows`: of the rows, and float32 of the weights."""
+    st = lib.purlin_combine_rows_backward(ctx.handle, _addr(dy), lddy, _addr(rows), ldr,
+                                          _addr(weights), _addr(place), _addr(drows), lddr,
+                                          _addr(dweights), tokens, top_k, cols, n_rows, dtype)
+    if st:
+        _ok(st, "purlin_combine_rows_backward")
 
 
 def purlin_empty_launch(stream=None):

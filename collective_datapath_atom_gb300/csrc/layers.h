@@ -1,5 +1,7 @@
 // layers.h -- host-side interface to the layer operators' kernels: the RMS
-// norm (rms_norm.cu) and the products grouped by expert (grouped.cu).
+// norm (rms_norm.cu), the norms around a block (block_norm.cu), the router
+// (router.cu), the rows' way to their experts and back (expert_rows.cu) and
+// the products grouped by expert (grouped.cu).
 // Internal to the library.
 #pragma once
 
@@ -72,6 +74,119 @@ struct NormBackwardArgs {
 cudaError_t launch_norm(const NormArgs &a);
 size_t norm_backward_workspace(const NormBackwardArgs &a);
 cudaError_t launch_norm_backward(const NormBackwardArgs &a);
+
+// ---------------------------------------------------- norms around a block --
+
+struct BlockNormArgs {
+    const void *x = nullptr;
+    const void *post_weight = nullptr;   // or null
+    const void *gate = nullptr;          // or null
+    const void *residual = nullptr;      // or null
+    const void *weight = nullptr;        // or null, with y
+    void *y = nullptr;
+    void *total = nullptr;               // or null
+    float *scales = nullptr;             // e4m3 output only
+    size_t ldx = 0, ldg = 0, ldr = 0, ldy = 0, ldt = 0;
+    bool gate_rows = false;              // a gate an element, else a column
+    float block_scale = 1, residual_scale = 1;
+    size_t rows = 0, hidden = 0;
+    float eps = 0;
+    int dtype = 0, out_dtype = 0;
+    int sms = 0;
+    unsigned long long *err = nullptr;
+    cudaStream_t stream = nullptr;
+};
+
+struct BlockNormBackwardArgs {
+    const void *dy = nullptr;            // or null, with total, weight and dweight
+    const void *dtotal = nullptr;        // or null
+    const void *x = nullptr;
+    const void *total = nullptr;
+    const void *post_weight = nullptr;   // or null
+    const void *gate = nullptr;          // or null
+    const void *weight = nullptr;
+    void *dx = nullptr;
+    void *dresidual = nullptr;           // or null
+    float *dpost_weight = nullptr;
+    void *dgate = nullptr;               // f32 columns, or rows in dtype
+    float *dweight = nullptr;
+    float *partial = nullptr;            // block_norm_backward_workspace() bytes
+    size_t lddy = 0, lddt = 0, ldx = 0, ldt = 0, ldg = 0, lddx = 0, lddr = 0, lddg = 0;
+    bool gate_rows = false;
+    float block_scale = 1, residual_scale = 1;
+    size_t rows = 0, hidden = 0;
+    float eps = 0;
+    int dtype = 0;
+    int sms = 0;
+    unsigned long long *err = nullptr;
+    cudaStream_t stream = nullptr;
+};
+
+cudaError_t launch_block_norm(const BlockNormArgs &a);
+size_t block_norm_backward_workspace(const BlockNormBackwardArgs &a);
+cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs &a);
+
+// ------------------------------------------------------------------ router --
+
+constexpr int kMaxChoices = 32;        // a lane of a warp each
+constexpr int kMaxExpertGroups = 32;   // at least a lane each
+
+struct RouteArgs {
+    const void *logits = nullptr;
+    const float *bias = nullptr;        // or null
+    const float *dweights = nullptr;    // backward
+    float *weights = nullptr;           // forward
+    int32_t *chosen = nullptr;          // forward: written; backward: read
+    void *dlogits = nullptr;            // backward
+    size_t ld = 0, ldd = 0, tokens = 0;
+    int experts = 0, top_k = 0, groups = 1, top_groups = 1, group_top = 1;
+    bool sigmoid = false, renormalise = false;
+    float scale = 1;
+    int dtype = 0;
+    int sms = 0;
+    cudaStream_t stream = nullptr;
+};
+
+cudaError_t launch_route(const RouteArgs &a);
+cudaError_t launch_route_backward(const RouteArgs &a);
+
+// ---------------------------------------------- rows to their experts, back --
+
+struct OrderArgs {
+    const int32_t *chosen = nullptr;
+    int32_t *place = nullptr;
+    int64_t *begin = nullptr;
+    int64_t *count = nullptr;
+    int *partial = nullptr;   // expert_order_workspace() bytes
+    size_t slots = 0, capacity = 0;
+    int groups = 0;
+    int sms = 0;
+    cudaStream_t stream = nullptr;
+};
+
+size_t expert_order_workspace(const OrderArgs &a);   // 0: none
+cudaError_t launch_expert_order(const OrderArgs &a);
+
+struct RowsArgs {
+    const void *x = nullptr;            // dispatch: the tokens' rows; backward: dy
+    const void *rows = nullptr;         // combine and backward: the experts' rows
+    const void *shared = nullptr;       // combine: or null
+    const float *scales = nullptr;      // dispatch: or null
+    const float *weights = nullptr;     // combine: or null
+    const int32_t *place = nullptr;
+    void *out = nullptr;                // dispatch: out; combine: y; backward: drows
+    float *out_scales = nullptr;        // dispatch, with scales; backward: dweights
+    size_t ldx = 0, ldr = 0, lds = 0, ldo = 0;
+    size_t tokens = 0, cols = 0, n_rows = 0;   // n_rows: of the experts' side
+    int top_k = 0;
+    int dtype = 0;
+    int sms = 0;
+    cudaStream_t stream = nullptr;
+};
+
+cudaError_t launch_dispatch_rows(const RowsArgs &a);
+cudaError_t launch_combine_rows(const RowsArgs &a);
+cudaError_t launch_combine_rows_backward(const RowsArgs &a);
 
 // ------------------------------------------------------ grouped products --
 

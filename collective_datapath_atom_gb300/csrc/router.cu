@@ -1,0 +1,521 @@
+// router.cu -- which experts a token goes to, and with what weights: scores of its
+// logits (softmax or sigmoid), a bias for balance, groups of experts, the top k, and
+// their renormalised weights; and the weights' gradient with respect to the logits.
+//
+// A warp has a token.  Its lanes are dealt out to the groups of experts, 32 / P lanes
+// a group (P: the groups, rounded up to a power of two), and each lane holds
+// consecutive experts of its group, so that a lower lane holds lower experts: an
+// expert's key is its choice value as an ordered 32-bit number, the largest key of the
+// warp is one reduction, and of equal keys the lowest lane's is the lowest expert.
+//
+// The choice is that of exact values.  Without a bias the scores rise with the logits,
+// and the logits themselves are compared, exactly.  With one, binary32 values c carry
+// an error of at most `tol`, and where two that matter to the answer (neighbours among
+// the chosen, the last of them and what is left, the last group kept and the rest) are
+// no further apart than that, and not of the same logit and bias, what is near the
+// border is computed again in binary64 and ranked by that: about one row in a thousand.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "layers.h"
+
+namespace purlin {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kMaxFinite = 3.40282347e38f;
+constexpr int kRouteWarps = 8;   // tokens of a block
+
+__device__ __forceinline__ float minus_infinity() { return __int_as_float(0xff800000); }
+
+struct RouteParams {
+    const void *logits;
+    const float *bias, *dweights;
+    float *weights;
+    int32_t *chosen;
+    void *dlogits;
+    size_t ld, ldd, tokens;
+    int experts, top_k, groups, top_groups, group_top;
+    int each;    // experts of a group
+    int lanes;   // lanes of a group
+    int held;    // experts of a lane
+    bool sigmoid, renormalise;
+    float scale;
+};
+
+__device__ __forceinline__ float value_of(const float *p) { return *p; }
+__device__ __forceinline__ float value_of(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// A logit as it counts: +inf is the largest finite value, -0 is 0, NaN is NaN.
+__device__ __forceinline__ float counted(float l) { return (l > kMaxFinite ? kMaxFinite : l) + 0.f; }
+
+// Numbers in the order of the values; 0 is left for "none".
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float sigmoid_of(float l) {
+    const float z = expf(-fabsf(l));
+    return (l >= 0.f ? 1.f : z) / (1.f + z);
+}
+
+// The choice value in binary64: a score and the bias.
+struct Exact {
+    bool sigmoid;
+    double most, sum;   // softmax: the largest logit, and the sum of exp(l - most)
+    __device__ __noinline__ double operator()(float l, float b) const {
+        const double d = (double)l;
+        if (sigmoid) {
+            const double z = exp(-fabs(d));
+            return (d >= 0 ? 1.0 : z) / (1.0 + z) + (double)b;
+        }
+        return exp(d - most) / sum + (double)b;
+    }
+};
+
+// One row's experts as a lane holds them: `n` of them from `first` on.
+template <typename T, int HELD>
+struct Row {
+    const T *logits;
+    const float *bias;
+    int first, n;
+    __device__ __forceinline__ float logit(int e) const { return counted(value_of(logits + e)); }
+    __device__ __forceinline__ float bias_at(int e) const { return bias ? bias[e] + 0.f : 0.f; }
+};
+
+// Binary64's denominators of a row's scores.
+template <typename T, int HELD>
+__device__ __noinline__ Exact exact_scores(const Row<T, HELD> &row, bool sigmoid, float most) {
+    Exact x{sigmoid, (double)most, 1.0};
+    if (!sigmoid) {
+        double s = 0;
+        for (int i = 0; i < row.n; ++i) {
+            const float l = row.logit(row.first + i);
+            if (l >= -kMaxFinite) s += exp((double)l - x.most);
+        }
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        x.sum = s;
+    }
+    return x;
+}
+
+// Whether this lane's group is kept, by binary64 values.
+template <typename T, int HELD>
+__device__ __noinline__ bool exact_groups(const Row<T, HELD> &row, const uint32_t (&key)[HELD],
+                                          const Exact &exact, const RouteParams &p, int lane) {
+    double a = -INFINITY, b = -INFINITY;   // the lane's two largest
+#pragma unroll 1
+    for (int i = 0; i < row.n; ++i) {
+        bool in = false;
+#pragma unroll
+        for (int q = 0; q < HELD; ++q) in |= q == i && key[q] != 0;
+        if (!in) continue;
+        const double d = exact(row.logit(row.first + i), row.bias_at(row.first + i));
+        if (d > a) {
+            b = a;
+            a = d;
+        } else if (d > b) {
+            b = d;
+        }
+    }
+    for (int o = 1; o < p.lanes; o <<= 1) {
+        const double oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+        b = fmax(fmin(a, oa), fmax(b, ob));
+        a = fmax(a, oa);
+    }
+    const double v = p.group_top == 2 && b > -INFINITY ? a + b : a;
+    int rank = 0;
+    const int g = lane / p.lanes;
+    for (int h = 0; h < p.groups; ++h) {
+        const double o = __shfl_sync(kAll, v, h * p.lanes);
+        rank += o > v || (o == v && h < g);
+    }
+    return g < p.groups && rank < p.top_groups && a > -INFINITY;
+}
+
+template <typename T, int HELD>
+__global__ void __launch_bounds__(32 * kRouteWarps)
+route_kernel(const __grid_constant__ RouteParams p) {
+    const int lane = threadIdx.x & 31;
+    const size_t token = (size_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+    if (token >= p.tokens) return;   // whole warps
+    const int g = lane / p.lanes, sub = lane - g * p.lanes;
+    Row<T, HELD> row;
+    row.logits = static_cast<const T *>(p.logits) + token * p.ld;
+    row.bias = p.bias;
+    row.first = g * p.each + sub * p.held;
+    row.n = g < p.groups ? max(0, min(p.held, p.each - sub * p.held)) : 0;
+
+    float l[HELD];
+    uint32_t key[HELD];
+    bool bad = false;   // a NaN in the row
+    float most = minus_infinity();
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        l[i] = i < row.n ? value_of(row.logits + row.first + i) : minus_infinity();
+        if (l[i] != l[i]) {
+            bad = true;
+            l[i] = minus_infinity();
+        }
+        l[i] = counted(l[i]);
+        most = fmaxf(most, l[i]);
+    }
+    bad = __any_sync(kAll, bad);
+    most = warp_max(most);
+    const bool some = most >= -kMaxFinite;   // an expert at all
+    float inv = 0.f;                         // softmax: 1 / the sum of exp(l - most)
+    if (!p.sigmoid && some && (p.bias || !p.renormalise || p.group_top == 2)) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) s += expf(l[i] - most);
+        inv = 1.f / warp_sum(s);
+    }
+    // an error of the choice values: of the scores, none above the largest one, and of a
+    // sum's rounding.  Sigmoid: exp 2, the sum and the quotient 1 ulp; softmax: those, and
+    // HELD + 5 additions
+    const float largest = p.sigmoid ? sigmoid_of(most) : inv;
+    const float tol = largest * (p.sigmoid ? 0x1p-20f : (float)(HELD + 16) * 0x1p-22f) + 0x1p-120f;
+    auto near = [&](float hi, float lo, float by) {   // not told apart, infinities too
+        return !(hi - lo > by + fabsf(hi) * 0x1p-22f);
+    };
+    auto score = [&](float v) { return p.sigmoid ? sigmoid_of(v) : expf(v - most) * inv; };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        if (p.bias) {
+            const float c = i < row.n ? score(l[i]) + row.bias_at(row.first + i) : 0.f;
+            key[i] = l[i] >= -kMaxFinite && c > minus_infinity() ? key_of(c) : 0;
+        } else {
+            key[i] = l[i] >= -kMaxFinite ? key_of(l[i]) : 0;
+        }
+    }
+
+    if (p.top_groups < p.groups) {
+        uint32_t a = 0, b = 0;   // the group's two largest keys
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            b = max(b, min(a, key[i]));
+            a = max(a, key[i]);
+        }
+        for (int o = 1; o < p.lanes; o <<= 1) {
+            const uint32_t oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+            b = max(min(a, oa), max(b, ob));
+            a = max(a, oa);
+        }
+        float v = of_key(a);
+        const bool exactly = !p.bias && p.group_top == 1;   // logits, nothing to tell apart
+        if (!exactly) {
+            if (!p.bias) v = score(v);
+            if (p.group_top == 2 && b != 0) v += p.bias ? of_key(b) : score(of_key(b));
+        }
+        const uint32_t mine = a != 0 ? key_of(v) : 0;
+        int rank = 0;
+        for (int h = 0; h < p.groups; ++h) {
+            const uint32_t o = __shfl_sync(kAll, mine, h * p.lanes);
+            rank += o > mine || (o == mine && h < g);
+        }
+        const bool there = g < p.groups && mine != 0;
+        bool keep = there && rank < p.top_groups;
+        if (!exactly) {
+            // the last one kept, and whether another one near it is not its like
+            const unsigned last = __ballot_sync(kAll, there && rank == p.top_groups - 1);
+            if (last != 0) {
+                const int at = __ffs(last) - 1;
+                const float edge = __shfl_sync(kAll, v, at);
+                const uint32_t ea = __shfl_sync(kAll, a, at), eb = __shfl_sync(kAll, b, at);
+                const bool close =
+                    there && near(fmaxf(v, edge), fminf(v, edge), 2.f * tol + fabsf(edge) * 0x1p-22f);
+                const bool alike = !p.bias && a == ea && b == eb;
+                if (__any_sync(kAll, close && !keep) && __any_sync(kAll, close && !alike && rank != p.top_groups - 1))
+                    keep = exact_groups(row, key, exact_scores(row, p.sigmoid, most), p, lane);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (!keep) key[i] = 0;
+    }
+
+    // the largest key of the warp, top_k times; lane j keeps the j-th
+    uint32_t best = 0;
+    int best_i = 0;
+    auto rescan = [&] {
+        best = 0;
+#pragma unroll
+        for (int i = HELD - 1; i >= 0; --i)
+            if (key[i] >= best) {
+                best = key[i];
+                best_i = i;
+            }
+    };
+    rescan();
+    uint32_t my_key = 0;
+    int my_e = -1, n = 0;
+    auto take = [&] {
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        if (top == 0) return false;
+        const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
+        const int e = __shfl_sync(kAll, row.first + best_i, from);
+        if (lane == n) {
+            my_key = top;
+            my_e = e;
+        }
+        ++n;
+        if (lane == from) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if (i == best_i) key[i] = 0;
+            rescan();
+        }
+        return true;
+    };
+    while (n < p.top_k && take()) {
+    }
+    float my_l = my_e >= 0 ? row.logit(my_e) : minus_infinity();
+
+    if (p.bias && n > 0) {
+        const float my_b = my_e >= 0 ? row.bias_at(my_e) : 0.f;
+        const float c = of_key(my_key);
+        const float next_c = __shfl_down_sync(kAll, c, 1);
+        const float next_l = __shfl_down_sync(kAll, my_l, 1), next_b = __shfl_down_sync(kAll, my_b, 1);
+        bool unsure = lane + 1 < n && near(c, next_c, 2.f * tol) && !(my_l == next_l && my_b == next_b);
+        const float edge = __shfl_sync(kAll, c, n - 1);
+        const float edge_l = __shfl_sync(kAll, my_l, n - 1), edge_b = __shfl_sync(kAll, my_b, n - 1);
+        int close = 0;   // of what is left, as near to the last one chosen
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            if (key[i] != 0 && near(edge, of_key(key[i]), 2.f * tol)) {
+                ++close;
+                unsure |= !(l[i] == edge_l && row.bias_at(row.first + i) == edge_b);
+            }
+        }
+        if (__any_sync(kAll, unsure)) {
+            const Exact exact = exact_scores(row, p.sigmoid, most);
+            const int chosen = n, all = chosen + __reduce_add_sync(kAll, close);
+            if (all <= 32) {
+                // a candidate a lane, each at its rank among them
+                while (n < all && take()) {
+                }
+                const double d = my_e >= 0 ? exact(row.logit(my_e), row.bias_at(my_e)) : -INFINITY;
+                int rank = 0;
+                for (int i = 0; i < n; ++i) {
+                    const double o = __shfl_sync(kAll, d, i);
+                    const int oe = __shfl_sync(kAll, my_e, i);
+                    rank += o > d || (o == d && oe < my_e);
+                }
+                int e = -1;
+                for (int i = 0; i < n; ++i) {
+                    const int r = __shfl_sync(kAll, rank, i), oe = __shfl_sync(kAll, my_e, i);
+                    if (r == lane) e = oe;
+                }
+                my_e = lane < chosen ? e : -1;
+            } else {
+                // every expert that is left, by binary64 values, one after another
+                for (int j = 0; j < chosen; ++j) {
+                    const int e = __shfl_sync(kAll, my_e, j);
+#pragma unroll
+                    for (int i = 0; i < HELD; ++i)
+                        if (i < row.n && row.first + i == e) key[i] = 1;
+                }
+                for (int j = 0; j < chosen; ++j) {
+                    double most_d = -INFINITY;
+                    int at = 0x7fffffff;
+#pragma unroll 1
+                    for (int i = 0; i < row.n; ++i) {
+                        bool in = false;
+#pragma unroll
+                        for (int q = 0; q < HELD; ++q) in |= q == i && key[q] != 0;
+                        if (!in) continue;
+                        const double d = exact(row.logit(row.first + i), row.bias_at(row.first + i));
+                        if (at == 0x7fffffff || d > most_d) {
+                            most_d = d;
+                            at = row.first + i;
+                        }
+                    }
+                    for (int o = 16; o > 0; o >>= 1) {
+                        const double od = __shfl_xor_sync(kAll, most_d, o);
+                        const int oa = __shfl_xor_sync(kAll, at, o);
+                        if (od > most_d || (od == most_d && oa < at)) {
+                            most_d = od;
+                            at = oa;
+                        }
+                    }
+                    if (lane == j) my_e = at;
+#pragma unroll
+                    for (int i = 0; i < HELD; ++i)
+                        if (i < row.n && row.first + i == at) key[i] = 0;
+                }
+            }
+            n = chosen;
+            my_l = my_e >= 0 ? row.logit(my_e) : minus_infinity();
+        }
+    }
+
+    const bool mine = lane < n;
+    float w = 0.f;
+    if (p.renormalise) {
+        // over the chosen logits alone, by a factor that keeps the largest from being small
+        const float top = warp_max(mine ? my_l : minus_infinity());
+        if (p.sigmoid) {
+            if (mine) w = expf(fminf(my_l, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(my_l)));
+        } else if (mine) {
+            w = expf(my_l - top);
+        }
+        const float s = warp_sum(w);
+        w = s > 0.f ? w / s : 0.f;
+    } else if (mine) {
+        w = score(my_l);
+    }
+    if (lane < p.top_k) {
+        const size_t at = token * p.top_k + lane;
+        p.weights[at] = bad ? __int_as_float(0x7fffffff) : w * p.scale;
+        p.chosen[at] = mine ? my_e : -1;
+    }
+}
+
+// ---------------------------------------------------------------- backward --
+
+// A warp a token: the chosen experts' shares in the lanes, then the row.  Without
+// renormalisation a softmax has a gradient for every expert; else the row is zeros but
+// for the chosen ones.
+template <typename T>
+__global__ void __launch_bounds__(32 * kRouteWarps)
+route_backward_kernel(const __grid_constant__ RouteParams p) {
+    const int lane = threadIdx.x & 31;
+    const size_t token = (size_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+    if (token >= p.tokens) return;   // whole warps
+    const T *row = static_cast<const T *>(p.logits) + token * p.ld;
+    T *out = static_cast<T *>(p.dlogits) + token * p.ldd;
+    int e = -1;
+    float l = minus_infinity(), g = 0.f;
+    if (lane < p.top_k) {
+        const size_t at = token * p.top_k + lane;
+        e = p.chosen[at];
+        if ((unsigned)e < (unsigned)p.experts) {
+            l = counted(value_of(row + e));
+            g = p.scale * p.dweights[at];
+        } else {
+            e = -1;
+        }
+    }
+    const bool real = e >= 0 && l >= -kMaxFinite;
+    const bool dense = !p.sigmoid && !p.renormalise;
+    float v = 0.f, total = 0.f, most = 0.f, inv = 0.f;
+    if (p.renormalise) {
+        const float top = warp_max(real ? l : minus_infinity());
+        float n = 0.f;
+        if (real)
+            n = p.sigmoid ? expf(fminf(l, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(l)))
+                          : expf(l - top);
+        const float s = warp_sum(n), share = s > 0.f ? n / s : 0.f;
+        const float mean = warp_sum(real ? g * share : 0.f);
+        if (real) v = share * (g - mean) * (p.sigmoid ? sigmoid_of(-l) : 1.f);
+    } else if (p.sigmoid) {
+        if (real) v = g * sigmoid_of(l) * sigmoid_of(-l);
+    } else {
+        most = minus_infinity();
+        for (int i = lane; i < p.experts; i += 32) most = fmaxf(most, counted(value_of(row + i)));
+        most = warp_max(most);
+        float s = 0.f;
+        if (most >= -kMaxFinite)
+            for (int i = lane; i < p.experts; i += 32) s += expf(counted(value_of(row + i)) - most);
+        s = warp_sum(s);
+        inv = s == 0.f ? 0.f : 1.f / s;   // (NaN for a row with a NaN)
+        const float share = real ? expf(l - most) * inv : 0.f;
+        total = warp_sum(real ? g * share : 0.f);
+        v = real ? g * share : 0.f;
+        l = share;   // (the score, from here on)
+    }
+    // an expert that occurs twice: its shares' sum, in both of its lanes
+    const unsigned alike = __match_any_sync(kAll, e);
+    if (__any_sync(kAll, e >= 0 && __popc(alike) > 1)) {
+        float sum = 0.f;
+        for (int i = 0; i < p.top_k; ++i) {
+            const float o = __shfl_sync(kAll, v, i);
+            if (alike >> i & 1) sum += o;
+        }
+        v = sum;
+    }
+    if (dense && real) v -= l * total;
+    __syncwarp();   // dlogits may be logits: every lane has read its chosen one
+    for (int i = lane; i < p.experts; i += 32) {
+        float d = 0.f;
+        if (dense && inv != 0.f) d = -expf(counted(value_of(row + i)) - most) * inv * total;
+        put(out + i, d);
+    }
+    __syncwarp();
+    if (e >= 0) put(out + e, v);
+}
+
+RouteParams params(const RouteArgs &a) {
+    RouteParams p{};
+    p.logits = a.logits;
+    p.bias = a.bias;
+    p.dweights = a.dweights;
+    p.weights = a.weights;
+    p.chosen = a.chosen;
+    p.dlogits = a.dlogits;
+    p.ld = a.ld;
+    p.ldd = a.ldd;
+    p.tokens = a.tokens;
+    p.experts = a.experts;
+    p.top_k = a.top_k;
+    p.groups = a.groups;
+    p.top_groups = a.top_groups;
+    p.group_top = a.groups > 1 && a.top_groups < a.groups ? a.group_top : 1;
+    p.each = a.experts / a.groups;
+    int pow2 = 1;
+    while (pow2 < a.groups) pow2 *= 2;
+    p.lanes = 32 / pow2;
+    p.held = (p.each + p.lanes - 1) / p.lanes;
+    p.sigmoid = a.sigmoid;
+    p.renormalise = a.renormalise;
+    p.scale = a.scale;
+    return p;
+}
+
+template <typename T>
+cudaError_t route_typed(const RouteArgs &a) {
+    const RouteParams p = params(a);
+    const unsigned grid = (unsigned)((a.tokens + kRouteWarps - 1) / kRouteWarps);
+    constexpr int kBlock = 32 * kRouteWarps;
+    if (p.held <= 1) route_kernel<T, 1><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (p.held <= 2) route_kernel<T, 2><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (p.held <= 4) route_kernel<T, 4><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (p.held <= 8) route_kernel<T, 8><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (p.held <= 16) route_kernel<T, 16><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (p.held <= 32) route_kernel<T, 32><<<grid, kBlock, 0, a.stream>>>(p);
+    else route_kernel<T, 64><<<grid, kBlock, 0, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs &a) {
+    return a.dtype == PURLIN_F32 ? route_typed<float>(a) : route_typed<__nv_bfloat16>(a);
+}
+
+cudaError_t launch_route_backward(const RouteArgs &a) {
+    const RouteParams p = params(a);
+    const unsigned grid = (unsigned)((a.tokens + kRouteWarps - 1) / kRouteWarps);
+    if (a.dtype == PURLIN_F32) route_backward_kernel<float><<<grid, 32 * kRouteWarps, 0, a.stream>>>(p);
+    else route_backward_kernel<__nv_bfloat16><<<grid, 32 * kRouteWarps, 0, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace purlin

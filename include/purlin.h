@@ -266,7 +266,8 @@ purlin_status purlin_noalloc_check(purlin_stream stream);
 /* What a language model's layer computes directly after the collectives: the
  * norm that consumes an AllReduce (the residual's addition in it), and the
  * experts' products that consume an AllToAllV dispatch, each with its
- * backward pass.  They are calls on one rank's buffers; loop over the ranks
+ * backward pass; and what lies between them: norms around a block, the router,
+ * the order by expert, and the rows' way there and back.  They are calls on one rank's buffers; loop over the ranks
  * as the buffers are laid out.
  *
  * Shared conventions.  Matrices are row-major; `ld*` is the distance between
@@ -369,6 +370,187 @@ purlin_status purlin_grouped_matmul_weight_grad(purlin_ctx *ctx, const void *dy,
                                                 const int64_t begin[], const int64_t count[],
                                                 int groups, size_t rows, size_t n, size_t k,
                                                 purlin_dtype dtype);
+
+/* Norms after and before a block, with the gate and the residual's addition
+ * between them, for each row:
+ *   u = x / sqrt(mean(x^2) + eps) * post_weight     (post_weight NULL: u = x)
+ *   t = residual_scale * residual + block_scale * gate * u
+ *   v = t / sqrt(mean(t^2) + eps) * weight
+ * x is the block's output (an AllReduce's, or purlin_combine_rows'), v the
+ * next block's input.  residual NULL: that term is 0; gate NULL: 1.  gate has
+ * a value a column, the same for every row (PURLIN_GATE_COLUMNS; ldg is
+ * ignored), or one an element (PURLIN_GATE_ROWS, rows x hidden).  y is v in
+ * dtype, or in E4M3 with scales[row], as in purlin_rms_norm; total (or NULL)
+ * receives t.  weight and y NULL: t alone is wanted; out_dtype is then dtype.
+ * Both norms are of unrounded values: t is rounded only as total.
+ * dtype F32 or BF16, that of every input and of total.  Pointers need only
+ * their type's alignment; rows on 16-byte boundaries take 128-bit accesses.
+ * total may be x or residual, and y may be x or residual when the types are
+ * equal (same pointer and ld).  rows == 0 is a no-op.
+ * Errors: INVALID_ARG (NULL, hidden 0, ld < hidden, eps negative or not
+ * finite, a scale not finite, scales given or missing, y without weight,
+ * neither y nor total), UNSUPPORTED (other out_dtype), ALIGNMENT, ALIAS, CUDA. */
+typedef enum {
+    PURLIN_GATE_COLUMNS = 0,   /* hidden values, for every row alike */
+    PURLIN_GATE_ROWS = 1       /* rows x hidden values */
+} purlin_gate_layout;
+
+purlin_status purlin_block_norm(purlin_ctx *ctx, const void *x, size_t ldx,
+                                const void *post_weight, const void *gate, size_t ldg,
+                                purlin_gate_layout gate_layout, float block_scale,
+                                const void *residual, size_t ldr, float residual_scale,
+                                const void *weight, void *y, size_t ldy, void *total, size_t ldt,
+                                float *scales, size_t rows, size_t hidden, float eps,
+                                purlin_dtype dtype, purlin_dtype out_dtype);
+
+/* Gradient of purlin_block_norm at x and t = total (as the forward pass left
+ * it).  dy: gradient of y; dtotal: gradient of total from the layers above,
+ * or NULL.  With r = 1 / sqrt(mean(t^2) + eps), q = 1 / sqrt(mean(x^2) + eps):
+ *   dt = r * (dy * weight - t * r^2 * mean(dy * weight * t)) + dtotal
+ *   dresidual = residual_scale * dt
+ *   h = block_scale * dt * gate * post_weight
+ *   dx = q * (h - x * q^2 * mean(h * x))            (post_weight NULL: dx = h)
+ *   dweight[j] = sum over rows of dy * t * r
+ *   dpost_weight[j] = sum over rows of block_scale * dt * gate * x * q
+ *   dgate = block_scale * dt * u                    (COLUMNS: summed over rows)
+ * dweight, dpost_weight and a COLUMNS dgate are F32, overwritten; a ROWS
+ * dgate is rows x hidden in dtype.  dpost_weight and dgate are given exactly
+ * where post_weight and gate are; dresidual may be NULL.  weight NULL (t alone
+ * was wanted): dy, total and dweight are NULL, and dtotal is given.
+ * dx, dresidual and a ROWS dgate may each be one of dy, total, dtotal, x and a
+ * ROWS gate (same pointer and ld).  rows == 0 sets the F32 gradients to zero.
+ * Errors as for purlin_block_norm, plus OOM (workspace) and UNSUPPORTED during
+ * capture (above). */
+purlin_status purlin_block_norm_backward(purlin_ctx *ctx, const void *dy, size_t lddy,
+                                         const void *dtotal, size_t lddt, const void *x,
+                                         size_t ldx, const void *total, size_t ldt,
+                                         const void *post_weight, const void *gate, size_t ldg,
+                                         purlin_gate_layout gate_layout, float block_scale,
+                                         float residual_scale, const void *weight, void *dx,
+                                         size_t lddx, void *dresidual, size_t lddr,
+                                         float *dpost_weight, void *dgate, size_t lddg,
+                                         float *dweight, size_t rows, size_t hidden, float eps,
+                                         purlin_dtype dtype);
+
+/* Routing of tokens to experts.  The router's logits come from a product of
+ * the normed rows; what it answers goes to the dispatch below. */
+typedef enum { PURLIN_SOFTMAX = 0, PURLIN_SIGMOID = 1 } purlin_scores;
+
+typedef struct purlin_router {
+    int32_t experts;      /* 1..PURLIN_MAX_GROUPS */
+    int32_t top_k;        /* experts a token goes to: 1..32, at most what the kept groups hold */
+    int32_t scores;       /* purlin_scores */
+    int32_t groups;       /* groups of experts / groups neighbours; 0 or 1: one group; at most 32 */
+    int32_t top_groups;   /* groups kept (ignored with one group) */
+    int32_t group_top;    /* a group's value is the sum of its 1 or 2 largest choices (0: 1) */
+    int32_t renormalise;  /* 1: the chosen scores are divided by their sum */
+    float scale;          /* of the weights; 0: 1 */
+} purlin_router;
+
+/* For each token, from its row of `experts` logits l (F32 or BF16):
+ *   s = softmax(l) or sigmoid(l);  c = s + bias     (bias NULL: c = s)
+ * The groups are ranked by the sum of their group_top largest c (of those
+ * there are) and top_groups kept; of the kept groups' experts the top_k
+ * largest c are chosen.  chosen[token][j] is the j-th of them (falling c) and
+ *   weights[token][j] = scale * s[chosen] (/ the sum of the chosen s).
+ * The bias (F32, `experts` values) evens out the load: it decides the choice
+ * and is not in the weights.  The choice is that of exact values: where
+ * binary32 does not tell two apart, binary64 does; equal values go to the
+ * lowest index.  Renormalised weights are those of the logits, also where the
+ * scores themselves would be too small for binary32.
+ * Masks: an expert whose logit is -inf has score 0 and is not chosen, nor is
+ * one whose bias is -inf or NaN.  Where fewer than top_k are left, the last
+ * entries are -1 with weight 0 (all of a row's, if it has none).  +inf counts
+ * as the largest finite value.  A NaN logit is not chosen, and its row's
+ * weights are NaN.
+ * weights and chosen are contiguous, tokens x top_k, 4-byte aligned; logits
+ * need their type's alignment.  tokens == 0 is a no-op; tokens * top_k is at
+ * most 2^31 - 4096.
+ * Errors: INVALID_ARG (NULL, a router outside the ranges above, experts not a
+ * multiple of groups, scale not finite, ld < experts), UNSUPPORTED (group_top
+ * above 2; more than 32 groups or choices), ALIGNMENT, ALIAS, CUDA. */
+purlin_status purlin_route(purlin_ctx *ctx, const void *logits, size_t ld, const float *bias,
+                           float *weights, int32_t *chosen, size_t tokens,
+                           const purlin_router *router, purlin_dtype dtype);
+
+/* Gradient of purlin_route's weights with respect to the logits, for the
+ * experts `chosen` there.  With g = scale * dweights, 0 for an expert that is
+ * not chosen, and p the renormalised weights without scale:
+ *   softmax                 dl = s * (g - sum(g * s))
+ *   softmax, renormalised   dl = p * (g - sum(g * p))
+ *   sigmoid                 dl = s * (1 - s) * g
+ *   sigmoid, renormalised   dl = p * (1 - s) * (g - sum(g * p))
+ * dlogits, in dtype, is written whole (zeros included), and may be logits
+ * (same pointer and ld).  Entries of `chosen` outside 0 .. experts - 1 count
+ * as none; one that occurs twice in a row counts as one with the sum of its g
+ * (not renormalised), or as two (renormalised).  tokens == 0 is a no-op.
+ * Errors as for purlin_route. */
+purlin_status purlin_route_backward(purlin_ctx *ctx, const float *dweights, const void *logits,
+                                    size_t ld, const int32_t *chosen, void *dlogits, size_t ldd,
+                                    size_t tokens, const purlin_router *router,
+                                    purlin_dtype dtype);
+
+/* The order of slots by expert.  chosen holds `slots` expert numbers (a
+ * token's top_k one after another); with capacity 0, slot i goes to row
+ *   place[i] = begin[e] + (slots before i of the same expert),  e = chosen[i]
+ *   count[e] = slots of expert e,  begin[e] = sum of the counts before e
+ * so that the experts' rows lie packed, one expert after another.  With a
+ * capacity, begin[e] = e * capacity, and slots past the capacity-th of their
+ * expert are dropped: place -1, and not counted.  Numbers outside 0 ..
+ * groups - 1 are dropped too.  begin and count (int64, 8-byte aligned,
+ * `groups` of them) are what purlin_grouped_matmul takes; count is a row of
+ * AllToAllV's device counts.  groups <= PURLIN_MAX_GROUPS; slots and
+ * groups * capacity are at most 2^31 - 4096.  slots == 0 sets count to zero
+ * (begin as above); groups == 0 sets every place to -1.
+ * Errors: INVALID_ARG (NULL, ranges), ALIGNMENT, ALIAS, OOM (workspace),
+ * UNSUPPORTED during capture (above), CUDA. */
+purlin_status purlin_expert_order(purlin_ctx *ctx, const int32_t *chosen, int32_t *place,
+                                  int64_t *begin, int64_t *count, size_t slots, int groups,
+                                  size_t capacity);
+
+/* Rows to their places: out[place[t * top_k + j]] = x[t] for every token t and
+ * j < top_k, a copy of `cols` elements of dtype F32, BF16 or E4M3, and
+ * out_scales[place] = scales[t] where both are given (F32, a scale a row).
+ * Places outside 0 .. out_rows - 1 are skipped; rows of out that no place
+ * names are left as they were; places must differ from one another (which of
+ * two equal ones is left is not said).  x and out need their type's alignment;
+ * rows on 16-byte boundaries move 16 bytes at a time.  top_k is 1..32; tokens
+ * or cols == 0 is a no-op.  The gradient of x is purlin_combine_rows of out's
+ * gradient, without weights.
+ * Errors: INVALID_ARG (NULL, ranges, one of scales and out_scales without the
+ * other), ALIGNMENT, ALIAS, CUDA. */
+purlin_status purlin_dispatch_rows(purlin_ctx *ctx, const void *x, size_t ldx,
+                                   const float *scales, const int32_t *place, void *out,
+                                   size_t ldo, float *out_scales, size_t tokens, int top_k,
+                                   size_t cols, size_t out_rows, purlin_dtype dtype);
+
+/* The way back: for every token t
+ *   y[t] = shared[t] + sum over j of weights[t][j] * rows[place[t][j]]
+ * added in the order shared, j = 0, 1, ... in binary32 and rounded once.
+ * weights (F32, tokens x top_k, contiguous) NULL: 1; shared (the rows of
+ * experts that every token goes to) NULL: 0.  Places outside 0 .. n_rows - 1
+ * are skipped, whatever their weight; a token without places gets its shared
+ * row, or zeros.  dtype F32 or BF16, that of rows, shared and y.  y may be
+ * shared (same pointer and ld).  tokens or cols == 0 is a no-op.
+ * Errors as for purlin_dispatch_rows, UNSUPPORTED for E4M3. */
+purlin_status purlin_combine_rows(purlin_ctx *ctx, const void *rows, size_t ldr,
+                                  const float *weights, const int32_t *place, const void *shared,
+                                  size_t lds, void *y, size_t ldy, size_t tokens, int top_k,
+                                  size_t cols, size_t n_rows, purlin_dtype dtype);
+
+/* Gradient of purlin_combine_rows (that of shared is dy itself):
+ *   drows[place[t][j]] = weights[t][j] * dy[t]
+ *   dweights[t][j] = sum over columns of dy[t] * rows[place[t][j]]
+ * dweights (F32) is 0 where the place is outside 0 .. n_rows - 1; rows of
+ * drows that no place names are left as they were.  Places must differ from
+ * one another.  drows may be rows (same pointer and ld).  tokens == 0 is a
+ * no-op; cols == 0 sets dweights to zero.  Errors as for
+ * purlin_combine_rows. */
+purlin_status purlin_combine_rows_backward(purlin_ctx *ctx, const void *dy, size_t lddy,
+                                           const void *rows, size_t ldr, const float *weights,
+                                           const int32_t *place, void *drows, size_t lddr,
+                                           float *dweights, size_t tokens, int top_k, size_t cols,
+                                           size_t n_rows, purlin_dtype dtype);
 
 /* ------------------------------------------------------------ measurement */
 
