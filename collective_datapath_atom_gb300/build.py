@@ -23,7 +23,7 @@ EXAMPLES_LIB = os.path.join(HERE, "libpurlin_examples.so")
 SOURCES = ["plan.cpp", "api.cpp", "device_api.cpp", "channel_api.cpp", "vcounts_api.cpp", "kernels.cu",
            "kernels_ragged.cu", "noalloc.cu", "vcounts.cu", "packets.cu",
            "layers_api.cpp", "block_api.cpp", "experts_api.cpp", "rms_norm.cu", "grouped.cu",
-           "block_norm.cu", "router.cu", "expert_rows.cu"]
+           "block_norm.cu", "block_norm_backward.cu", "router.cu", "expert_rows.cu"]
 EXAMPLE_SOURCES = ["device_examples.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

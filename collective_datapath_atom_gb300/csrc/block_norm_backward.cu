@@ -1,0 +1,615 @@
+// block_norm_backward.cu -- gradients of the norms around a block (block_norm.cu), with
+// n = dy weight and c = block_scale * post_weight * gate:
+//   dt = r (n - t r^2 mean(n t)) + dtotal,  h = c dt,  dx = q (h - x q^2 mean(h x)),
+// and the sums over rows  dweight = sum dy t r,  S = sum dt x q (gate):  of a column
+// gate and the weight after the block, dgate = block_scale post_weight S and
+// dpost_weight = block_scale gate S.  A thread owns the same columns in every row, so its
+// shares of the two sums stay in registers, are written once a block and added up over
+// the blocks in a fixed order by a second kernel: no atomics, the same bits every time.
+#include "block_rows.cuh"
+
+namespace purlin {
+namespace {
+
+constexpr size_t kDirectThreadsSm = 512;   // rows on the registers: threads an SM
+
+struct BlockBackwardParams {
+    const void *dy, *dtotal, *x, *total, *post, *gate, *weight;
+    void *dx, *dresidual, *dgate;   // dgate: rows, or null
+    float *partial;                 // gridDim.x rows for dweight, then as many for S
+    size_t lddy, lddt, ldx, ldt, ldg, lddx, lddr, lddg, rows;
+    uint32_t hidden, phase;
+    float block_scale, residual_scale, eps;
+    bool gate_rows, sums;           // sums: S is wanted
+    unsigned long long *err;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(1024)
+block_norm_backward_long_kernel(const __grid_constant__ BlockBackwardParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
+    __shared__ float sums[4][32];
+    float *pw = p.partial + (size_t)blockIdx.x * p.hidden;
+    float *ps = p.partial + ((size_t)gridDim.x + blockIdx.x) * p.hidden;
+    for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
+        if (p.weight) pw[e] = 0.f;
+        if (p.sums) ps[e] = 0.f;
+    }
+    const T *post = static_cast<const T *>(p.post), *w = static_cast<const T *>(p.weight);
+    for (size_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T *dy = static_cast<const T *>(p.dy) + row * p.lddy;
+        const T *total = static_cast<const T *>(p.total) + row * p.ldt;
+        const T *x = static_cast<const T *>(p.x) + row * p.ldx;
+        const T *dtotal = p.dtotal ? static_cast<const T *>(p.dtotal) + row * p.lddt : nullptr;
+        const T *gate = static_cast<const T *>(p.gate);
+        if (p.gate_rows) gate += row * p.ldg;
+        float xx = 0.f, tt = 0.f, nt = 0.f;
+        for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
+            if (post) {
+                const float v = to_f32<T>(x[e]);
+                xx = fmaf(v, v, xx);
+            }
+            if (w) {
+                const float t = to_f32<T>(total[e]);
+                tt = fmaf(t, t, tt);
+                nt = fmaf(to_f32<T>(dy[e]) * to_f32<T>(w[e]), t, nt);
+            }
+        }
+        xx = reduce_row<Sum>(xx, false, sums[0]);
+        tt = reduce_row<Sum>(tt, false, sums[1]);
+        nt = reduce_row<Sum>(nt, false, sums[2]);
+        const float q = post ? rsqrtf(xx / (float)p.hidden + p.eps) : 1.f;
+        const float r = w ? rsqrtf(tt / (float)p.hidden + p.eps) : 0.f;
+        const float c = r * r * (nt / (float)p.hidden);
+        auto dt_at = [&](uint32_t e) {
+            float d = dtotal ? to_f32<T>(dtotal[e]) : 0.f;
+            if (w) d += r * fmaf(to_f32<T>(dy[e]), to_f32<T>(w[e]), -(to_f32<T>(total[e]) * c));
+            return d;
+        };
+        auto factor = [&](uint32_t e) {   // of dt in h
+            float f = p.block_scale;
+            if (post) f *= to_f32<T>(post[e]);
+            if (gate) f *= to_f32<T>(gate[e]);
+            return f;
+        };
+        float k = 0.f;
+        if (post) {
+            float hx = 0.f;
+            for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x)
+                hx = fmaf(dt_at(e) * factor(e), to_f32<T>(x[e]), hx);
+            k = q * q * (reduce_row<Sum>(hx, false, sums[3]) / (float)p.hidden);
+        }
+        for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
+            // every input of an element is read before an output, which may be one, is written
+            const float dt = dt_at(e), f = factor(e), v = to_f32<T>(x[e]);
+            const float g = p.gate_rows ? to_f32<T>(gate[e]) : 1.f;
+            const float pe = post ? to_f32<T>(post[e]) : 1.f;
+            if (w) pw[e] = fmaf(to_f32<T>(dy[e]), to_f32<T>(total[e]) * r, pw[e]);
+            if (p.sums) ps[e] = fmaf(dt * g, v * q, ps[e]);
+            const float h = dt * f;
+            if (p.dresidual)
+                static_cast<T *>(p.dresidual)[row * p.lddr + e] = from_f32<T>(p.residual_scale * dt);
+            if (p.dgate)
+                static_cast<T *>(p.dgate)[row * p.lddg + e] =
+                    from_f32<T>(p.block_scale * dt * (v * q * pe));
+            static_cast<T *>(p.dx)[row * p.lddx + e] = from_f32<T>(post ? q * fmaf(-v, k, h) : h);
+        }
+        __syncthreads();   // before the next row's sums
+    }
+}
+
+// Rows on the registers, for few of them: a thread holds ITEMS windows of V elements of
+// a row's h and x, and the sums over rows of its columns.  The operands are read for the
+// first sums, and again, from the caches, for dt and h.
+template <typename T, int V, int ITEMS, bool EDGE, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
+    __shared__ float sums[4][2][32];   // rows take turns
+    __shared__ float joined[2][32 * ITEMS * V];
+    const bool warp_only = blockDim.x == 32;
+    const size_t step = (size_t)gridDim.x * blockDim.y;
+    size_t row = (size_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int hidden = (int)p.hidden, estep = (int)blockDim.x * V;
+    const T *gates = p.gate_rows ? static_cast<const T *>(p.gate) : nullptr;
+    const bool normed = p.weight != nullptr;
+    const int e0 = (int)threadIdx.x * V - (EDGE ? phase_of<V>(p.phase, p.ldx, row) : 0);   // (the grid keeps the phase)
+    const float inv_hidden = 1.f / (float)hidden;
+    float acc_w[ITEMS][V] = {}, acc_s[ITEMS][V] = {};
+    for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+        auto read = [&](const void *base, size_t ld, int i) {
+            return read_window<T, V, EDGE>(static_cast<const T *>(base) + row * ld, e0 + i * estep, hidden);
+        };
+        auto weight = [&](int i) {
+            return read_weight<T, V, EDGE>(static_cast<const T *>(p.weight), e0 + i * estep, hidden);
+        };
+        float xx = 0.f, tt = 0.f, nt = 0.f;
+        Window<T, V> xs[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) xs[i] = read(p.x, p.ldx, i);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if (normed) {
+                const Window<T, V> tk = read(p.total, p.ldt, i), gk = read(p.dy, p.lddy, i), wk = weight(i);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    tt = fmaf(tk.at(j), tk.at(j), tt);
+                    nt = fmaf(gk.at(j) * wk.at(j), tk.at(j), nt);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) xx = fmaf(xs[i].at(j), xs[i].at(j), xx);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            xx += __shfl_xor_sync(0xffffffffu, xx, o);
+            tt += __shfl_xor_sync(0xffffffffu, tt, o);
+            nt += __shfl_xor_sync(0xffffffffu, nt, o);
+        }
+        if (!warp_only) {
+            const int warps = (int)blockDim.x >> 5;
+            if ((threadIdx.x & 31) == 0) {
+                sums[0][turn][threadIdx.x >> 5] = xx;
+                sums[1][turn][threadIdx.x >> 5] = tt;
+                sums[2][turn][threadIdx.x >> 5] = nt;
+            }
+            __syncthreads();
+            xx = tt = nt = 0.f;
+            for (int k = 0; k < warps; ++k) {
+                xx += sums[0][turn][k];
+                tt += sums[1][turn][k];
+                nt += sums[2][turn][k];
+            }
+        }
+        const float q = p.post ? rsqrtf(mean_of(xx, (float)hidden, inv_hidden) + p.eps) : 1.f;
+        const float r = normed ? rsqrtf(mean_of(tt, (float)hidden, inv_hidden) + p.eps) : 0.f;
+        const float c = r * r * mean_of(nt, (float)hidden, inv_hidden);
+        float h[ITEMS][V], hx = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int e = e0 + i * estep;
+            float dt[V], f[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) dt[j] = 0.f;
+            if (p.dtotal) {
+                const Window<T, V> dk = read(p.dtotal, p.lddt, i);
+#pragma unroll
+                for (int j = 0; j < V; ++j) dt[j] = dk.at(j);
+            }
+            Window<T, V> kk;
+            if (gates) kk = read(gates, p.ldg, i);
+            if (normed) {
+                const Window<T, V> tk = read(p.total, p.ldt, i), gk = read(p.dy, p.lddy, i), wk = weight(i);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float u = tk.at(j), d = gk.at(j);
+                    acc_w[i][j] = fmaf(d, u * r, acc_w[i][j]);
+                    dt[j] = fmaf(r, fmaf(d, wk.at(j), -(u * c)), dt[j]);
+                }
+            }
+            // outputs may be inputs: an element's were all read above
+            if (p.dresidual) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[j] = p.residual_scale * dt[j];
+                write_window<T, V, EDGE>(static_cast<T *>(p.dresidual) + row * p.lddr, e, hidden, f);
+            }
+            read_factor<T, V, EDGE>(p.post, p.gate_rows ? nullptr : p.gate, p.block_scale, e, hidden, f);
+            if (p.dgate) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[i][j] = dt[j] * (f[j] * (xs[i].at(j) * q));
+                write_window<T, V, EDGE>(static_cast<T *>(p.dgate) + row * p.lddg, e, hidden, h[i]);
+            }
+            if (gates) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) dt[j] *= kk.at(j);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                acc_s[i][j] = fmaf(dt[j], xs[i].at(j) * q, acc_s[i][j]);
+                h[i][j] = dt[j] * f[j];
+                hx = fmaf(h[i][j], xs[i].at(j), hx);
+            }
+        }
+        float k = 0.f;
+        if (p.post)
+            k = q * q * mean_of(reduce_row<Sum>(hx, warp_only, sums[3][turn]), (float)hidden, inv_hidden);
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if (p.post) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[i][j] = q * fmaf(-xs[i].at(j), k, h[i][j]);
+            }
+            write_window<T, V, EDGE>(dx, e0 + i * estep, hidden, h[i]);
+        }
+    }
+    float *pw = p.partial + (size_t)blockIdx.x * hidden;
+    float *ps = p.partial + ((size_t)gridDim.x + blockIdx.x) * hidden;
+    if (blockDim.y > 1) {   // the warps' sums, warp by warp
+        for (unsigned y = 0; y < blockDim.y; ++y) {
+            if (threadIdx.y == y) {
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int e = e0 + i * estep + j;
+                        if (e >= 0 && e < hidden) {
+                            joined[0][e] = y == 0 ? acc_w[i][j] : joined[0][e] + acc_w[i][j];
+                            joined[1][e] = y == 0 ? acc_s[i][j] : joined[1][e] + acc_s[i][j];
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+        for (int e = (int)(threadIdx.y * blockDim.x + threadIdx.x); e < hidden; e += (int)(blockDim.x * blockDim.y)) {
+            if (normed) pw[e] = joined[0][e];
+            if (p.sums) ps[e] = joined[1][e];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = e0 + i * estep + j;
+            if (e < 0 || e >= hidden) continue;
+            if (normed) pw[e] = acc_w[i][j];
+            if (p.sums) ps[e] = acc_s[i][j];
+        }
+}
+
+// A thread holds ITEMS windows of its row, and the sums over rows of its columns.  HOLD:
+// all of the operands' windows, so that the stage is free behind the first sums'
+// barrier; else (wide rows, more windows a thread) they are read from the stage again,
+// and x's and h's alone are held behind the second one.
+// The rows are normed (dy, total and the weight are there).  Arrays of a stage: x, dy,
+// total, the gates where there are any, and dtotal.
+struct TeamParams : BlockBackwardParams {
+    const void *src[5];
+    size_t ld[5];
+};
+
+template <typename T, int V, int ITEMS, bool EDGE, bool GATES, bool HOLD>
+__global__ void __launch_bounds__(kTeamThreads)
+block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __grid_constant__ TeamPlan plan) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
+    __shared__ uint64_t full[kTeamWarps][kMaxStages];
+    // rows take turns
+    __shared__ __align__(16) float sums[2][kTeamWarps][3][kTeamWarps], last[2][kTeamWarps][kTeamWarps];
+    const Team team(plan.warps);
+    const int teams = (int)blockDim.x / team.threads(), hidden = (int)p.hidden;
+    const int phase = EDGE ? phase_of<V>(p.phase, p.ldx, blockIdx.x) : 0;
+    const Vectors<T, V, ITEMS, EDGE> vectors(plan, p.weight, p.post, GATES ? nullptr : p.gate, p.block_scale,
+                                             hidden, phase, team);
+    constexpr int kDtotal = GATES ? 4 : 3;
+    const size_t row0 = blockIdx.x + (size_t)team.index * gridDim.x, step = (size_t)teams * gridDim.x;
+    TeamRing<T, V, 5, ITEMS, EDGE, TeamParams> ring(p, plan, team, full[team.index], vectors.end, phase, hidden, row0, step);
+    for (int i = threadIdx.x; i < (int)(sizeof(sums) / sizeof(float)); i += (int)blockDim.x) {
+        (&sums[0][0][0][0])[i] = 0.f;
+        if (i < (int)(sizeof(last) / sizeof(float))) (&last[0][0][0])[i] = 0.f;
+    }
+    ring.start();
+    vectors.start();
+    __syncthreads();
+    const float inv_hidden = 1.f / (float)hidden;
+    F2 acc_w[ITEMS][V / 2] = {}, acc_s[ITEMS][V / 2] = {};
+    int turn = 0;
+    for (size_t row = row0; row < p.rows; row += step, turn ^= 1) {
+        ring.wait();
+        constexpr int kHeld = HOLD ? ITEMS : 1;
+        Window<T, V> xs[ITEMS], gk[kHeld], tk[kHeld], dk[kHeld], kk[kHeld];
+        F2 xx = 0, tt = 0, nt = 0;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int h = HOLD ? i : 0;
+            xs[i] = ring.window(0, i);
+            gk[h] = ring.window(1, i);
+            tk[h] = ring.window(2, i);
+            if constexpr (HOLD) {
+                if constexpr (GATES) kk[h] = ring.window(3, i);
+                if (p.dtotal) dk[h] = ring.window(kDtotal, i);
+            }
+            const Window<T, V> wk = vectors.weights(i);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 u = pair_of(tk[h], j);
+                xx = fma2(pair_of(xs[i], j), pair_of(xs[i], j), xx);
+                tt = fma2(u, u, tt);
+                nt = fma2(mul2(pair_of(gk[h], j), pair_of(wk, j)), u, nt);
+            }
+        }
+        float sx = low(xx) + high(xx), st = low(tt) + high(tt), sn = low(nt) + high(nt);
+        team.sums(sx, st, sn, sums[turn][team.index]);
+        auto refill = [&] {   // behind a barrier: every thread has its share of the row
+            if (team.warps == 1) __syncwarp();
+            ring.refill();
+        };
+        if constexpr (HOLD) refill();
+        const float q = p.post ? rsqrtf(sx * inv_hidden + p.eps) : 1.f;
+        const float r = rsqrtf(st * inv_hidden + p.eps);
+        const float c = r * r * r * (sn * inv_hidden);
+        F2 h[ITEMS][V / 2], hx = 0;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int n = HOLD ? i : 0, e = vectors.column(i);
+            if constexpr (!HOLD) {
+                gk[n] = ring.window(1, i);
+                tk[n] = ring.window(2, i);
+                if constexpr (GATES) kk[n] = ring.window(3, i);
+                if (p.dtotal) dk[n] = ring.window(kDtotal, i);
+            }
+            const Window<T, V> wk = vectors.weights(i);
+            F2 dt[V / 2], f[V / 2];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {   // r dy weight - c t, and dy t r for dweight
+                const F2 u = pair_of(tk[n], j), d = mul2(pair_of(gk[n], j), both(r));
+                acc_w[i][j] = fma2(d, u, acc_w[i][j]);
+                dt[j] = fma2(d, pair_of(wk, j), mul2(u, both(-c)));
+            }
+            if (p.dtotal) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) dt[j] = add2(dt[j], pair_of(dk[n], j));
+            }
+            if (p.dresidual) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) f[j] = mul2(dt[j], both(p.residual_scale));
+                write_pairs<T, V, EDGE>(static_cast<T *>(p.dresidual) + row * p.lddr, e, hidden, f);
+            }
+            vectors.factor(i, f);
+            if constexpr (GATES) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    h[i][j] = mul2(dt[j], mul2(f[j], mul2(pair_of(xs[i], j), both(q))));
+                    dt[j] = mul2(dt[j], pair_of(kk[n], j));
+                }
+                write_pairs<T, V, EDGE>(static_cast<T *>(p.dgate) + row * p.lddg, e, hidden, h[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 u = pair_of(xs[i], j);
+                acc_s[i][j] = fma2(dt[j], mul2(u, both(q)), acc_s[i][j]);
+                h[i][j] = mul2(dt[j], f[j]);
+                hx = fma2(h[i][j], u, hx);
+            }
+        }
+        float k = 0.f;
+        if (p.post)
+            k = q * q * (team.template total<Sum>(low(hx) + high(hx), last[turn][team.index]) * inv_hidden);
+        else if constexpr (!HOLD)
+            team.sync();
+        if constexpr (!HOLD) refill();
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if (p.post) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j)
+                    h[i][j] = mul2(fma2(pair_of(xs[i], j), both(-k), h[i][j]), both(q));
+            }
+            write_pairs<T, V, EDGE>(dx, vectors.column(i), hidden, h[i]);
+        }
+        ring.settle();
+        if (EDGE && plan.stages == 1) team.sync();   // the next row's ends are read at once
+        ring.next();
+    }
+    if (team.thread == 0) ring.drain();
+    float *pw = p.partial + (size_t)blockIdx.x * hidden;
+    float *ps = p.partial + ((size_t)gridDim.x + blockIdx.x) * hidden;
+    auto each = [&](auto to) {   // the thread's columns and their sums
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = vectors.column(i) + j;
+                if (e >= 0 && e < hidden)
+                    to(e, j % 2 ? high(acc_w[i][j / 2]) : low(acc_w[i][j / 2]),
+                       j % 2 ? high(acc_s[i][j / 2]) : low(acc_s[i][j / 2]));
+            }
+    };
+    if (teams == 1) {
+        each([&](int e, float w, float s) {
+            pw[e] = w;
+            if (p.sums) ps[e] = s;
+        });
+        return;
+    }
+    // the teams' sums, team by team, where the vectors and rows lay
+    float *joined = reinterpret_cast<float *>(smem());
+    for (int g = 0; g < teams; ++g) {
+        __syncthreads();
+        if (team.index == g)
+            each([&](int e, float w, float s) {
+                joined[e] = g == 0 ? w : joined[e] + w;
+                joined[hidden + e] = g == 0 ? s : joined[hidden + e] + s;
+            });
+    }
+    __syncthreads();
+    for (int e = (int)threadIdx.x; e < hidden; e += (int)blockDim.x) {
+        pw[e] = joined[e];
+        if (p.sums) ps[e] = joined[hidden + e];
+    }
+}
+
+constexpr int kJoinRows = 32;
+
+// The blocks' sums, added up in a fixed order: dweight, and from S the gradients of
+// the weight after the block and of a column gate.
+template <typename T>
+__global__ void __launch_bounds__(32 * kJoinRows)
+block_join_kernel(const float *partial, const T *post, const T *gate, float block_scale,
+                  float *dweight, float *dpost, float *dgate, uint32_t hidden, int parts) {
+    __shared__ float sums[kJoinRows][33];
+    const uint32_t e = blockIdx.x * 32 + threadIdx.x;
+    const bool second = blockIdx.y == (dweight ? 1 : 0);
+    if (second) partial += (size_t)parts * hidden;
+    // launched while the rows are still being worked on: wait for all of them
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float v = 0.f;
+    if (e < hidden) {
+#pragma unroll 8
+        for (int b = threadIdx.y; b < parts; b += kJoinRows) v += partial[(size_t)b * hidden + e];
+    }
+    sums[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.y != 0 || e >= hidden) return;
+    v = sums[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < kJoinRows; ++k) v += sums[k][threadIdx.x];
+    if (!second) {
+        dweight[e] = v;
+        return;
+    }
+    v *= block_scale;
+    if (dpost) dpost[e] = gate ? v * to_f32<T>(gate[e]) : v;
+    if (dgate) dgate[e] = post ? v * to_f32<T>(post[e]) : v;
+}
+
+// Whether the sum S over rows is wanted.
+bool wants_sums(const BlockNormBackwardArgs &a) {
+    return a.post_weight != nullptr || (a.gate != nullptr && !a.gate_rows);
+}
+
+// A backward launch: its shape, and whether it takes windows and meets edges.
+struct BlockBackwardShape : Shape {
+    TeamShape team;   // plan.warps 0: none
+    int team_items = 0;
+    bool windows = false, edge = false, wide = false;
+};
+
+constexpr int kBackwardHeld = 16;   // values of a thread
+
+template <typename T>
+BlockBackwardShape block_backward_shape(const BlockNormBackwardArgs &a) {
+    constexpr int V = 16 / sizeof(T);
+    constexpr size_t es = sizeof(T);
+    BlockBackwardShape s;
+    const void *gates = a.gate_rows ? a.gate : nullptr, *dgates = a.gate_rows ? a.dgate : nullptr;
+    s.windows = in_step<V>(a.dy, a.lddy, es, a.x, a.ldx, es) &&
+                in_step<V>(a.total, a.ldt, es, a.x, a.ldx, es) &&
+                in_step<V>(a.dtotal, a.lddt, es, a.x, a.ldx, es) &&
+                in_step<V>(gates, a.ldg, es, a.x, a.ldx, es) &&
+                in_step<V>(a.dx, a.lddx, es, a.x, a.ldx, es) &&
+                in_step<V>(a.dresidual, a.lddr, es, a.x, a.ldx, es) &&
+                in_step<V>(dgates, a.lddg, es, a.x, a.ldx, es);
+    const bool edge = reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx % V != 0 || a.hidden % V != 0;
+    s.edge = edge;
+    for (const void *v : {a.post_weight, a.gate_rows ? nullptr : a.gate, a.weight})
+        s.edge = s.edge || reinterpret_cast<uintptr_t>(v) % 16 != 0;
+    Shape &base = s;
+    if (s.windows && a.weight) {
+        const int arrays = 3 + (a.dtotal ? 1 : 0) + (gates ? 1 : 0);
+        const bool factors = a.post_weight || (a.gate && !a.gate_rows);
+        for (s.team_items = 2; s.team_items <= 32 / V; s.team_items *= 2) {
+            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, s.team_items, true, a.sms);
+            s.grid = s.team.grid;
+            if (s.team.plan.warps != 0) return s;
+        }
+    }
+    for (unsigned threads : {512u, 1024u}) {
+        base = s.windows ? direct_shape<V>(a.rows, a.hidden, edge, kBackwardHeld, threads, a.sms)
+                         : direct_shape<1>(a.rows, a.hidden, false, kBackwardHeld, threads, a.sms);
+        s.wide = threads > 512;
+        if (s.items != 0) break;
+    }
+    if (s.items == 0) {   // the long kernel
+        s.grid = (unsigned)std::min<size_t>(a.rows, (size_t)a.sms * 2);
+        return s;
+    }
+    // blocks that fit at once, a multiple of the windows' elements so that a block's rows
+    // share their phase, or a row a block
+    if (s.ty > 1) s.ty = 4;
+    const size_t fit = std::max<size_t>(1, kDirectThreadsSm / (s.tx * s.ty));
+    const size_t grid = std::max<size_t>((size_t)a.sms * fit / V * V, V);
+    s.grid = (unsigned)std::min<size_t>((a.rows + s.ty - 1) / s.ty, grid);
+    return s;
+}
+
+template <typename T, int V, int ITEMS, bool EDGE, bool GATES>
+cudaError_t backward_teams(const BlockNormBackwardArgs &a, const TeamParams &p, const TeamShape &s) {
+    constexpr bool HOLD = ITEMS == 2;
+    static SharedMemoryLimit limit;
+    const cudaError_t ready =
+        limit.raise(block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD>, kTeamSmem);
+    if (ready != cudaSuccess) return ready;
+    block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD><<<s.grid, s.threads, s.smem, a.stream>>>(p, s.plan);
+    return cudaGetLastError();
+}
+
+template <typename T, int V, bool EDGE, bool GATES>
+cudaError_t backward_teams(const BlockNormBackwardArgs &a, const BlockBackwardParams &b,
+                           const BlockBackwardShape &s) {
+    const TeamParams p{b, {a.x, a.dy, a.total, GATES ? a.gate : a.dtotal, a.dtotal},
+                       {a.ldx, a.lddy, a.ldt, GATES ? a.ldg : a.lddt, a.lddt}};
+    if (s.team_items == 2) return backward_teams<T, V, 2, EDGE, GATES>(a, p, s.team);
+    if (s.team_items == 4) return backward_teams<T, V, 4, EDGE, GATES>(a, p, s.team);
+    if constexpr (V == 4) return backward_teams<T, V, 8, EDGE, GATES>(a, p, s.team);
+    return cudaErrorInvalidConfiguration;
+}
+
+template <typename T, int V>
+cudaError_t backward_direct(const BlockNormBackwardArgs &a, const BlockBackwardParams &p,
+                            const BlockBackwardShape &s) {
+    constexpr bool EDGE = V > 1;
+    constexpr int MOST = kBackwardHeld / V;
+    const dim3 block(s.tx, s.ty);
+    if (s.items == 0) block_norm_backward_long_kernel<T><<<s.grid, 1024, 0, a.stream>>>(p);
+    else if (s.wide) block_norm_backward_kernel<T, V, MOST, EDGE, 1024><<<s.grid, block, 0, a.stream>>>(p);
+    else if (s.items == 1) block_norm_backward_kernel<T, V, 1, EDGE, 512><<<s.grid, block, 0, a.stream>>>(p);
+    else if (s.items == MOST) block_norm_backward_kernel<T, V, MOST, EDGE, 512><<<s.grid, block, 0, a.stream>>>(p);
+    else if constexpr (V == 4) block_norm_backward_kernel<T, V, 2, EDGE, 512><<<s.grid, block, 0, a.stream>>>(p);
+    else if constexpr (V == 1) block_norm_backward_kernel<T, V, 4, EDGE, 512><<<s.grid, block, 0, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t block_norm_backward_any(const BlockNormBackwardArgs &a) {
+    constexpr int V = 16 / sizeof(T);
+    const bool sums = wants_sums(a);
+    const BlockBackwardShape s = block_backward_shape<T>(a);
+    const BlockBackwardParams p{a.dy, a.dtotal, a.x, a.total, a.post_weight, a.gate, a.weight,
+                                a.dx, a.dresidual, a.gate_rows ? a.dgate : nullptr, a.partial,
+                                a.lddy, a.lddt, a.ldx, a.ldt, a.ldg, a.lddx, a.lddr, a.lddg, a.rows,
+                                (uint32_t)a.hidden,
+                                (uint32_t)(reinterpret_cast<uintptr_t>(a.x) / sizeof(T) % V),
+                                a.block_scale, a.residual_scale, a.eps, a.gate_rows, sums, a.err};
+    const cudaError_t e = s.team.plan.warps != 0
+                              ? a.gate_rows ? s.edge ? backward_teams<T, V, true, true>(a, p, s)
+                                                     : backward_teams<T, V, false, true>(a, p, s)
+                                : s.edge    ? backward_teams<T, V, true, false>(a, p, s)
+                                            : backward_teams<T, V, false, false>(a, p, s)
+                          : s.windows ? backward_direct<T, V>(a, p, s)
+                                      : backward_direct<T, 1>(a, p, s);
+    const unsigned vectors = (a.weight ? 1 : 0) + (sums ? 1 : 0);
+    if (e != cudaSuccess || vectors == 0) return e;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)((a.hidden + 31) / 32), vectors);
+    c.blockDim = dim3(32, kJoinRows);
+    c.stream = a.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, block_join_kernel<T>, (const float *)a.partial,
+                              static_cast<const T *>(a.post_weight),
+                              a.gate_rows ? (const T *)nullptr : static_cast<const T *>(a.gate),
+                              a.block_scale, a.dweight, a.dpost_weight,
+                              a.gate_rows ? (float *)nullptr : static_cast<float *>(a.dgate),
+                              (uint32_t)a.hidden, (int)s.grid);
+}
+
+}  // namespace
+
+size_t block_norm_backward_workspace(const BlockNormBackwardArgs &a) {
+    if (a.weight == nullptr && !wants_sums(a)) return 0;
+    const unsigned grid = a.dtype == PURLIN_F32 ? block_backward_shape<float>(a).grid
+                                                : block_backward_shape<__nv_bfloat16>(a).grid;
+    return 2 * (size_t)grid * a.hidden * sizeof(float);
+}
+
+cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs &a) {
+    return a.dtype == PURLIN_F32 ? block_norm_backward_any<float>(a)
+                                 : block_norm_backward_any<__nv_bfloat16>(a);
+}
+
+}  // namespace purlin
