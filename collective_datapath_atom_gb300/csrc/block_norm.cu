@@ -154,8 +154,12 @@ block_norm_kernel(const __grid_constant__ BlockParams p) {
     }
 }
 
-// A thread holds ITEMS windows of its row's operands, so that the ring's stage is free
-// for another row behind the first sum's barrier.
+// A thread holds ITEMS windows of its row's t, made behind the first sum's barrier from
+// operands that it reads from the stage again.  Holding those, which frees the stage a
+// barrier earlier, needs 128 registers, and three teams of seven warps are worth more
+// than early loads: TEAMS3.
+constexpr int kForwardWarps = 21;
+
 // Operands of the rows, in the order of their arrays in a stage: x, the gates where
 // there are any, and the residual.
 struct TeamParams : BlockParams {
@@ -164,10 +168,10 @@ struct TeamParams : BlockParams {
 };
 
 template <typename T, typename O, int V, int ITEMS, bool EDGE, bool GATES>
-__global__ void __launch_bounds__(kTeamThreads)
+__global__ void __launch_bounds__(32 * kForwardWarps)
 block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_constant__ TeamPlan plan) {
-    __shared__ uint64_t full[kTeamWarps][kMaxStages];
-    __shared__ __align__(16) float sums[3][2][kTeamWarps][kTeamWarps];   // rows take turns
+    __shared__ uint64_t full[kForwardWarps][kMaxStages];
+    __shared__ __align__(16) float sums[3][2][kTeams][kTeamWarps];   // rows take turns; single warps have none
     const Team team(plan.warps);
     const int hidden = (int)p.hidden, phase = EDGE ? phase_of<V>(p.phase, p.ldx, blockIdx.x) : 0;
     const Vectors<T, V, ITEMS, EDGE> vectors(plan, p.weight, p.post, GATES ? nullptr : p.gate, p.block_scale,
@@ -176,6 +180,7 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
     const size_t step = (size_t)(blockDim.x / team.threads()) * gridDim.x;
     TeamRing<T, V, 3, ITEMS, EDGE, TeamParams> ring(p, plan, team, full[team.index], vectors.end, phase, hidden, row0, step);
     constexpr int kResidual = GATES ? 2 : 1;
+    const int slot = team.warps == 1 ? 0 : team.index;
     for (int i = threadIdx.x; i < (int)(sizeof(sums) / sizeof(float)); i += (int)blockDim.x) (&sums[0][0][0][0])[i] = 0.f;
     ring.start();
     vectors.start();
@@ -184,38 +189,34 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
     int turn = 0;
     for (size_t row = row0; row < p.rows; row += step, turn ^= 1) {
         ring.wait();
-        Window<T, V> xk[ITEMS], rk[ITEMS], gk[GATES ? ITEMS : 1];
         F2 xx = 0, tt = 0;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            xk[i] = ring.window(0, i);
-            if (p.residual) rk[i] = ring.window(kResidual, i);
-            if constexpr (GATES) gk[i] = ring.window(1, i);
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) xx = fma2(pair_of(xk[i], j), pair_of(xk[i], j), xx);
-        }
-        auto refill = [&] {   // behind a barrier: every thread has its share of the row
-            if (team.warps == 1) __syncwarp();
-            ring.refill();
-        };
         float q = 1.f;
         if (p.post) {
-            q = rsqrtf(team.template total<Sum>(low(xx) + high(xx), sums[0][turn][team.index]) * inv_hidden + p.eps);
-            refill();
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const Window<T, V> xk = ring.window(0, i);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) xx = fma2(pair_of(xk, j), pair_of(xk, j), xx);
+            }
+            q = rsqrtf(team.template total<Sum>(low(xx) + high(xx), sums[0][turn][slot]) * inv_hidden + p.eps);
         }
         F2 t[ITEMS][V / 2];
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             F2 c[V / 2];
             vectors.factor(i, c);
+            const Window<T, V> xk = ring.window(0, i);
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                t[i][j] = mul2(mul2(pair_of(xk[i], j), both(q)), c[j]);
-                if constexpr (GATES) t[i][j] = mul2(t[i][j], pair_of(gk[i], j));
+            for (int j = 0; j < V / 2; ++j) t[i][j] = mul2(mul2(pair_of(xk, j), both(q)), c[j]);
+            if constexpr (GATES) {
+                const Window<T, V> gk = ring.window(1, i);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) t[i][j] = mul2(t[i][j], pair_of(gk, j));
             }
             if (p.residual) {
+                const Window<T, V> rk = ring.window(kResidual, i);
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) t[i][j] = fma2(both(p.residual_scale), pair_of(rk[i], j), t[i][j]);
+                for (int j = 0; j < V / 2; ++j) t[i][j] = fma2(both(p.residual_scale), pair_of(rk, j), t[i][j]);
             }
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) tt = fma2(t[i][j], t[i][j], tt);
@@ -225,10 +226,15 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) write_pairs<T, V, EDGE>(total, vectors.column(i), hidden, t[i]);
         }
-        if (p.y) {
+        // behind a barrier, the stage is free for another row
+        if (!p.y) {
+            team.sync();
+            ring.refill();
+        } else {
             const float r =
-                rsqrtf(team.template total<Sum>(low(tt) + high(tt), sums[1][turn][team.index]) * inv_hidden + p.eps);
-            if (!p.post) refill();
+                rsqrtf(team.template total<Sum>(low(tt) + high(tt), sums[1][turn][slot]) * inv_hidden + p.eps);
+            if (team.warps == 1) __syncwarp();
+            ring.refill();
             O *y = static_cast<O *>(p.y) + row * p.ldy;
             float most = 0.f;
 #pragma unroll
@@ -243,30 +249,27 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
             }
             if constexpr (sizeof(O) == 1) {
                 // fmaxf passes over NaN: the scale stays a number, the elements are NaN
-                float scale = fmaxf(team.template total<Max>(most, sums[2][turn][team.index]) / kE4m3Max, kScaleMin);
+                float scale = fmaxf(team.template total<Max>(most, sums[2][turn][slot]) / kE4m3Max, kScaleMin);
                 if (team.thread == 0) p.scales[row] = scale;
                 // the binary32 quotients, as divide_row has them
-                float up = 1.f;
                 if (scale < 0x1p-80f) {   // remainders would fall below the smallest value
-                    up = 0x1p64f;
-                    scale *= up;
+                    scale *= 0x1p64f;
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                        for (int j = 0; j < V / 2; ++j) t[i][j] = mul2(t[i][j], both(0x1p64f));
                 }
                 const float inv = 1.f / scale, d = scale <= kF32Max ? scale : 0.f;
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i) {
 #pragma unroll
                     for (int j = 0; j < V / 2; ++j) {
-                        F2 v = t[i][j];
-                        if (up != 1.f) v = mul2(v, both(up));
-                        const F2 first = mul2(v, both(inv));
-                        t[i][j] = fma2(fma2(first, both(-d), v), both(inv), first);
+                        const F2 first = mul2(t[i][j], both(inv));
+                        t[i][j] = fma2(fma2(first, both(-d), t[i][j]), both(inv), first);
                     }
                     write_pairs<O, V, EDGE>(y, vectors.column(i), hidden, t[i]);
                 }
             }
-        } else if (!p.post) {
-            team.sync();
-            refill();
         }
         ring.settle();
         if (EDGE && plan.stages == 1) team.sync();   // the next row's ends are read at once
@@ -292,7 +295,8 @@ cudaError_t try_teams(const BlockNormArgs &a, const BlockParams &b, bool *done) 
     const bool factors = a.post_weight || (a.gate && !GATES);
     const auto shape = [&](int items) {
         const TeamShape s =
-            team_shape<V>(a.rows, a.hidden, EDGE, arrays, a.y != nullptr, factors, items, false, a.sms);
+            team_shape<V>(a.rows, a.hidden, EDGE, arrays, a.y != nullptr, factors, items, false, kForwardWarps,
+                          sizeof(O) == 1 ? kForwardWarps : sizeof(T) == 2 ? 12 : 8, a.sms);
         *done = s.plan.warps != 0;
         return s;
     };

@@ -11,6 +11,7 @@
 namespace purlin {
 namespace {
 
+constexpr int kBackwardWarps = 16;         // of a block of teams
 constexpr size_t kDirectThreadsSm = 512;   // rows on the registers: threads an SM
 
 struct BlockBackwardParams {
@@ -270,18 +271,19 @@ struct TeamParams : BlockBackwardParams {
 };
 
 template <typename T, int V, int ITEMS, bool EDGE, bool GATES, bool HOLD>
-__global__ void __launch_bounds__(kTeamThreads)
+__global__ void __launch_bounds__(32 * kBackwardWarps)
 block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __grid_constant__ TeamPlan plan) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
-    __shared__ uint64_t full[kTeamWarps][kMaxStages];
+    __shared__ uint64_t full[kBackwardWarps][kMaxStages];
     // rows take turns
-    __shared__ __align__(16) float sums[2][kTeamWarps][3][kTeamWarps], last[2][kTeamWarps][kTeamWarps];
+    __shared__ __align__(16) float sums[2][kTeams][3][kTeamWarps], last[2][kTeams][kTeamWarps];
     const Team team(plan.warps);
     const int teams = (int)blockDim.x / team.threads(), hidden = (int)p.hidden;
     const int phase = EDGE ? phase_of<V>(p.phase, p.ldx, blockIdx.x) : 0;
     const Vectors<T, V, ITEMS, EDGE> vectors(plan, p.weight, p.post, GATES ? nullptr : p.gate, p.block_scale,
                                              hidden, phase, team);
     constexpr int kDtotal = GATES ? 4 : 3;
+    const int slot = team.warps == 1 ? 0 : team.index;   // of what the warps add up
     const size_t row0 = blockIdx.x + (size_t)team.index * gridDim.x, step = (size_t)teams * gridDim.x;
     TeamRing<T, V, 5, ITEMS, EDGE, TeamParams> ring(p, plan, team, full[team.index], vectors.end, phase, hidden, row0, step);
     for (int i = threadIdx.x; i < (int)(sizeof(sums) / sizeof(float)); i += (int)blockDim.x) {
@@ -319,7 +321,7 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
             }
         }
         float sx = low(xx) + high(xx), st = low(tt) + high(tt), sn = low(nt) + high(nt);
-        team.sums(sx, st, sn, sums[turn][team.index]);
+        team.sums(sx, st, sn, sums[turn][slot]);
         auto refill = [&] {   // behind a barrier: every thread has its share of the row
             if (team.warps == 1) __syncwarp();
             ring.refill();
@@ -374,7 +376,7 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         }
         float k = 0.f;
         if (p.post)
-            k = q * q * (team.template total<Sum>(low(hx) + high(hx), last[turn][team.index]) * inv_hidden);
+            k = q * q * (team.template total<Sum>(low(hx) + high(hx), last[turn][slot]) * inv_hidden);
         else if constexpr (!HOLD)
             team.sync();
         if constexpr (!HOLD) refill();
@@ -500,7 +502,8 @@ BlockBackwardShape block_backward_shape(const BlockNormBackwardArgs &a) {
         const int arrays = 3 + (a.dtotal ? 1 : 0) + (gates ? 1 : 0);
         const bool factors = a.post_weight || (a.gate && !a.gate_rows);
         for (s.team_items = 2; s.team_items <= 32 / V; s.team_items *= 2) {
-            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, s.team_items, true, a.sms);
+            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, s.team_items, true, kBackwardWarps,
+                                   kBackwardWarps, a.sms);
             s.grid = s.team.grid;
             if (s.team.plan.warps != 0) return s;
         }

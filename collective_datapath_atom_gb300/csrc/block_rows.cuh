@@ -9,7 +9,8 @@
 namespace purlin {
 namespace {
 
-constexpr int kTeamThreads = 512;             // most threads of a block of teams
+constexpr int kTeamWarps = 16;                // most warps of a team
+constexpr int kTeams = 15;                    // most teams of more than a warp: their barriers
 constexpr int kTeamSmem = 216 * 1024;         // most dynamic shared memory of one: 11 KiB are its own
 
 // The factor of x q in t for a window, block_scale * post_weight * column gate, in
@@ -118,8 +119,6 @@ __device__ __forceinline__ Window<T, V> staged_window(uint32_t at) {
 }
 
 // What the warps of a team add up: a float a warp, and zeros behind them.
-constexpr int kTeamWarps = kTeamThreads / 32;
-
 // Eight floats at once, as a tree.
 template <typename Op>
 __device__ __forceinline__ float join_eight(const float *shared) {
@@ -133,11 +132,14 @@ __device__ __forceinline__ float join_warps(const float *shared, int warps) {
 }
 
 struct Team {
-    int index, warps, thread;   // thread: within the team
+    // thread: within the team.  A thread's windows are every 32nd from window(ITEMS) on:
+    // a warp's lie together, and the distances are known to the compiler
+    int index, warps, thread;
     __device__ explicit Team(int warps)
         : index((int)(threadIdx.x >> 5) / warps), warps(warps),
           thread((int)threadIdx.x - index * warps * 32) {}
     __device__ int threads() const { return warps * 32; }
+    __device__ int window(int items) const { return (thread & ~31) * items + (thread & 31); }
     __device__ __forceinline__ void sync() const {
         if (warps == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(warps * 32) : "memory");
@@ -206,7 +208,7 @@ struct TeamRing {
           stage_bytes(plan.arrays * array_bytes), stages(plan.stages), arrays(plan.arrays), phase(phase),
           hidden(hidden), next_row(row0), step(step) {
         base = rings + team.index * stages * stage_bytes;
-        at = base + team.thread * 16;
+        at = base + team.window(ITEMS) * 16;
     }
     // Team thread 0: fill the stage at `fill` with the next row, if one is left.
     __device__ __forceinline__ void issue() {
@@ -292,11 +294,11 @@ struct TeamRing {
         if (++st == stages) {
             st = 0;
             parity ^= 1;
-            at = base + team.thread * 16;
+            at = base + team.window(ITEMS) * 16;
         }
     }
     __device__ __forceinline__ Window<T, V> window(int a, int i) const {
-        return staged_window<T, V>(at + a * array_bytes + i * team.threads() * 16);
+        return staged_window<T, V>(at + a * array_bytes + i * 512);
     }
     // Team thread 0, at the end: copies that a wait gave up on land before the exit.
     __device__ void drain() {
@@ -311,21 +313,23 @@ template <typename T, int V, int ITEMS, bool EDGE>
 struct Vectors {
     const void *weight, *post, *gate;
     float scale;
-    int hidden, threads, thread, e0;
-    uint32_t factor_at, end;   // from the start of shared memory, where the weight lies
+    int hidden, e0;
+    uint32_t weight_at, factor_at, end;   // this thread's, from the start of shared memory; behind them
     bool weight_staged, factor_staged, factors;
 
     __device__ Vectors(const TeamPlan &plan, const void *weight, const void *post, const void *gate, float scale,
                        int hidden, int phase, const Team &team)
-        : weight(weight), post(post), gate(gate), scale(scale), hidden(hidden), threads(team.threads()),
-          thread(team.thread), e0(team.thread * V - phase), weight_staged(plan.weight_staged),
+        : weight(weight), post(post), gate(gate), scale(scale), hidden(hidden),
+          e0(team.window(ITEMS) * V - phase), weight_staged(plan.weight_staged),
           factor_staged(plan.factor_staged), factors(post != nullptr || gate != nullptr) {
-        factor_at = weight_staged ? ITEMS * threads * 16 : 0;
-        end = factor_at + (factor_staged ? ITEMS * threads * V * 4 : 0);
+        const uint32_t weight_bytes = weight_staged ? ITEMS * team.threads() * 16 : 0;
+        weight_at = team.window(ITEMS) * 16;
+        factor_at = weight_bytes + team.window(ITEMS * (V / 4)) * 16;
+        end = weight_bytes + (factor_staged ? ITEMS * team.threads() * V * 4 : 0);
     }
-    __device__ __forceinline__ int column(int i) const { return e0 + i * threads * V; }
+    __device__ __forceinline__ int column(int i) const { return e0 + i * 32 * V; }
     __device__ __forceinline__ float4 *factor_quad(int i, int n) const {
-        return reinterpret_cast<float4 *>(smem() + factor_at + ((i * (V / 4) + n) * threads + thread) * 16);
+        return reinterpret_cast<float4 *>(smem() + factor_at + (i * (V / 4) + n) * 512);
     }
     // Every team writes the same; a block barrier follows.
     __device__ void start() const {
@@ -333,7 +337,7 @@ struct Vectors {
         for (int i = 0; i < ITEMS; ++i) {
             if (weight_staged) {
                 const Window<T, V> k = read_weight<T, V, EDGE>(static_cast<const T *>(weight), column(i), hidden);
-                *reinterpret_cast<uint4 *>(smem() + (i * threads + thread) * 16) = make_uint4(k.w[0], k.w[1], k.w[2], k.w[3]);
+                *reinterpret_cast<uint4 *>(smem() + weight_at + i * 512) = make_uint4(k.w[0], k.w[1], k.w[2], k.w[3]);
             }
             if (factor_staged) {
                 float c[V];
@@ -346,7 +350,7 @@ struct Vectors {
     }
     __device__ __forceinline__ Window<T, V> weights(int i) const {
         if (!weight_staged) return read_weight<T, V, EDGE>(static_cast<const T *>(weight), column(i), hidden);
-        return staged_window<T, V>((i * threads + thread) * 16);
+        return staged_window<T, V>(weight_at + i * 512);
     }
     __device__ __forceinline__ void factor(int i, F2 (&c)[V / 2]) const {
         if (factor_staged) {
@@ -398,17 +402,22 @@ struct TeamShape {
     size_t smem = 0;
 };
 
-// Teams with `items` windows a thread, `arrays` operands a stage.  As many teams as fit
-// and as there are rows for, each with two rows on their way at least; vectors that the
-// rows leave no room for are read from global memory, and last a ring has one stage.
+// Teams with `items` windows a thread, `arrays` operands a stage, and two stages at
+// least; vectors that the rows leave no room for are read from global memory, and last a
+// ring has one stage.  Teams: `least_warps` an SM, which the arithmetic wants, and rows
+// for about 100 KB on their way; reads that run further ahead of the writes slow both
+// down (forward 16384 x 4096 bf16: three teams of two stages, 98 KB, 91 us, four 104).
 // joins: the teams' sums over rows are added up in shared memory, two floats a column.
+// block_warps: of a block at most, 32 at most.
+constexpr size_t kTeamFlight = 100 * 1024, kRingFlight = 128 * 1024;
+
 template <int V>
 TeamShape team_shape(size_t rows, size_t hidden, bool edge, int arrays, bool weight, bool factors, int items,
-                     bool joins, int sms) {
+                     bool joins, int block_warps, int least_warps, int sms) {
     TeamShape s;
     if (rows < (size_t)sms) return s;
     const int warps = (int)(warps_of(windows_of<V>(hidden, edge), items) / 32);
-    if (warps > kTeamWarps) return s;
+    if (warps > kTeamWarps || warps > block_warps) return s;
     const size_t windows = (size_t)items * warps * 32;
     const size_t stage = windows * 16 * (size_t)arrays, room = kTeamSmem;
     for (int want = 2; want >= 1; --want)
@@ -416,10 +425,12 @@ TeamShape team_shape(size_t rows, size_t hidden, bool edge, int arrays, bool wei
             if (want == 1 && drop < 2) continue;   // the vectors go first
             const bool ws = weight && drop < 2, fs = factors && drop < 1;
             const size_t vectors = windows * ((ws ? 16 : 0) + (fs ? 4 * V : 0));
-            for (size_t teams = std::min<size_t>(kTeamWarps / warps, (rows + sms - 1) / sms); teams >= 1; --teams) {
+            const size_t some = std::max<size_t>((least_warps + warps - 1) / warps, kTeamFlight / (2 * stage));
+            for (size_t teams = std::min({some, (size_t)(block_warps / warps), (rows + sms - 1) / sms}); teams >= 1; --teams) {
                 if (vectors + teams * want * stage > room) continue;
                 if (joins && teams > 1 && vectors + teams * want * stage < 8 * hidden) continue;
-                const size_t stages = std::min<size_t>(kMaxStages, (room - vectors) / (teams * stage));
+                const size_t stages = std::min({(size_t)kMaxStages, (room - vectors) / (teams * stage),
+                                                std::max<size_t>(want, kRingFlight / (teams * stage))});
                 s.plan = TeamPlan{warps, (int)stages, arrays, ws, fs};
                 s.threads = (unsigned)(teams * warps * 32);
                 s.smem = vectors + teams * stages * stage;
