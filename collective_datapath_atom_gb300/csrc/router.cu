@@ -76,6 +76,16 @@ __device__ __forceinline__ float sigmoid_of(float l) {
     return (l >= 0.f ? 1.f : z) / (1.f + z);
 }
 
+// The same for the choice alone, by the approximate 2^x and 1 / x: off by 2 + 1.2 |l|
+// ulp of the exponential, which is as many of the score where that is small, and next
+// to none where it is near 1 (16384 x 256: with exp and a division 2 us more).
+__device__ __forceinline__ float choice_sigmoid(float l) {
+    float z, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(l * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + z));
+    return s;
+}
+
 // The choice value in binary64: a score and the bias.
 struct Exact {
     bool sigmoid;
@@ -98,6 +108,84 @@ struct Row {
     int first, n;
     __device__ __forceinline__ float logit(int e) const { return counted(value_of(logits + e)); }
     __device__ __forceinline__ float bias_at(int e) const { return bias ? bias[e] + 0.f : 0.f; }
+};
+
+// HELD consecutive values from 16-byte boundaries (fewer bytes where there are fewer).
+template <int HELD>
+__device__ __forceinline__ void load_held(float (&v)[HELD], const float *p) {
+    if constexpr (HELD % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < HELD / 4; ++i) {
+            const float4 u = reinterpret_cast<const float4 *>(p)[i];
+            v[4 * i] = u.x;
+            v[4 * i + 1] = u.y;
+            v[4 * i + 2] = u.z;
+            v[4 * i + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) v[i] = p[i];
+    }
+}
+template <int HELD>
+__device__ __forceinline__ void load_held(float (&v)[HELD], const __nv_bfloat16 *p) {
+    if constexpr (HELD % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < HELD / 8; ++i) {
+            const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) v[i] = __bfloat162float(p[i]);
+    }
+}
+
+// A lane's two largest keys and their places; experts that were taken are out of it.
+template <int HELD>
+struct Best {
+    using Mask = uint64_t;
+    uint32_t key = 0, second = 0;
+    int at = 0, second_at = 0;
+    Mask taken = 0;
+    __device__ __forceinline__ void scan(const uint32_t (&keys)[HELD]) {
+        key = second = 0;
+        at = second_at = 0;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const uint32_t k = (HELD <= 32 ? (uint32_t)taken >> i : (uint32_t)(taken >> i)) & 1 ? 0 : keys[i];
+            if (k > key) {
+                second = key;
+                second_at = at;
+                key = k;
+                at = i;
+            } else if (k > second) {
+                second = k;
+                second_at = i;
+            }
+        }
+    }
+    // The largest is taken; a lane that has given two looks for the rest again.
+    __device__ __forceinline__ void take(const uint32_t (&keys)[HELD]) {
+        taken |= (Mask)1 << at;
+        if (second != 0) {
+            key = second;
+            at = second_at;
+            second = 0;
+            fresh = false;
+        } else if (!fresh) {
+            scan(keys);
+            fresh = true;
+        } else {
+            key = 0;
+        }
+    }
+    bool fresh = true;   // the second largest is known, or there is none
 };
 
 // Binary64's denominators of a row's scores.
@@ -150,7 +238,8 @@ __device__ __noinline__ bool exact_groups(const Row<T, HELD> &row, const uint32_
     return g < p.groups && rank < p.top_groups && a > -INFINITY;
 }
 
-template <typename T, int HELD>
+// VECTOR: every lane holds HELD experts, on 16-byte boundaries.
+template <typename T, int HELD, bool VECTOR>
 __global__ void __launch_bounds__(32 * kRouteWarps)
 route_kernel(const __grid_constant__ RouteParams p) {
     const int lane = threadIdx.x & 31;
@@ -161,71 +250,78 @@ route_kernel(const __grid_constant__ RouteParams p) {
     row.logits = static_cast<const T *>(p.logits) + token * p.ld;
     row.bias = p.bias;
     row.first = g * p.each + sub * p.held;
-    row.n = g < p.groups ? max(0, min(p.held, p.each - sub * p.held)) : 0;
+    row.n = VECTOR ? HELD : g < p.groups ? max(0, min(p.held, p.each - sub * p.held)) : 0;
 
-    float l[HELD];
-    uint32_t key[HELD];
+    float l[HELD], b[HELD];
+    if constexpr (VECTOR) {
+        load_held<HELD>(l, row.logits + row.first);
+        if (p.bias) load_held<HELD>(b, p.bias + row.first);
+    } else {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            l[i] = i < row.n ? value_of(row.logits + row.first + i) : minus_infinity();
+            if (p.bias) b[i] = i < row.n ? p.bias[row.first + i] : 0.f;
+        }
+    }
     bool bad = false;   // a NaN in the row
     float most = minus_infinity();
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-        l[i] = i < row.n ? value_of(row.logits + row.first + i) : minus_infinity();
-        if (l[i] != l[i]) {
-            bad = true;
-            l[i] = minus_infinity();
-        }
-        l[i] = counted(l[i]);
-        most = fmaxf(most, l[i]);
+        bad |= l[i] != l[i];
+        most = fmaxf(most, l[i]);   // (not a NaN)
     }
     bad = __any_sync(kAll, bad);
-    most = warp_max(most);
-    const bool some = most >= -kMaxFinite;   // an expert at all
-    float inv = 0.f;                         // softmax: 1 / the sum of exp(l - most)
-    if (!p.sigmoid && some && (p.bias || !p.renormalise || p.group_top == 2)) {
+    most = counted(warp_max(most));
+    float inv = 0.f;   // softmax: 1 / the sum of exp(l - most)
+    const bool whole = !p.sigmoid && most >= -kMaxFinite && (p.bias || !p.renormalise || p.group_top == 2);
+    if (whole) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) s += expf(l[i] - most);
+        for (int i = 0; i < HELD; ++i) s += expf(counted(l[i]) - most);
         inv = 1.f / warp_sum(s);
+        if (bad) {   // (then the choice is of the rest)
+            s = 0.f;
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) s += l[i] == l[i] ? expf(counted(l[i]) - most) : 0.f;
+            inv = 1.f / warp_sum(s);
+        }
     }
-    // an error of the choice values: of the scores, none above the largest one, and of a
-    // sum's rounding.  Sigmoid: exp 2, the sum and the quotient 1 ulp; softmax: those, and
-    // HELD + 5 additions
-    const float largest = p.sigmoid ? sigmoid_of(most) : inv;
-    const float tol = largest * (p.sigmoid ? 0x1p-20f : (float)(HELD + 16) * 0x1p-22f) + 0x1p-120f;
+    // an error of the choice values: of the scores, none above the largest one's (l e^-l
+    // falls), and of a sum's rounding.  Softmax: the exponential, the quotient and HELD + 5
+    // additions
+    const float largest = p.sigmoid ? choice_sigmoid(most) : inv;
+    const float tol = largest * (p.sigmoid ? 4.f + 1.2f * fmaxf(-most, 0.f) : (float)(HELD + 16)) * 0x1p-22f + 0x1p-120f;
     auto near = [&](float hi, float lo, float by) {   // not told apart, infinities too
         return !(hi - lo > by + fabsf(hi) * 0x1p-22f);
     };
-    auto score = [&](float v) { return p.sigmoid ? sigmoid_of(v) : expf(v - most) * inv; };
+    auto score = [&](float v) { return p.sigmoid ? choice_sigmoid(v) : expf(v - most) * inv; };
+    uint32_t key[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-        if (p.bias) {
-            const float c = i < row.n ? score(l[i]) + row.bias_at(row.first + i) : 0.f;
-            key[i] = l[i] >= -kMaxFinite && c > minus_infinity() ? key_of(c) : 0;
-        } else {
-            key[i] = l[i] >= -kMaxFinite ? key_of(l[i]) : 0;
-        }
+        float c;
+        if (p.bias) c = score(p.sigmoid ? l[i] : counted(l[i])) + b[i];
+        else c = counted(l[i]);
+        key[i] = l[i] >= -kMaxFinite && c > minus_infinity() ? key_of(c) : 0;
     }
+    Best<HELD> best;
+    best.scan(key);
 
     if (p.top_groups < p.groups) {
-        uint32_t a = 0, b = 0;   // the group's two largest keys
-#pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            b = max(b, min(a, key[i]));
-            a = max(a, key[i]);
-        }
+        uint32_t a = best.key, c = best.second;   // the group's two largest keys
         for (int o = 1; o < p.lanes; o <<= 1) {
-            const uint32_t oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-            b = max(min(a, oa), max(b, ob));
+            const uint32_t oa = __shfl_xor_sync(kAll, a, o), oc = __shfl_xor_sync(kAll, c, o);
+            c = max(min(a, oa), max(c, oc));
             a = max(a, oa);
         }
         float v = of_key(a);
         const bool exactly = !p.bias && p.group_top == 1;   // logits, nothing to tell apart
         if (!exactly) {
             if (!p.bias) v = score(v);
-            if (p.group_top == 2 && b != 0) v += p.bias ? of_key(b) : score(of_key(b));
+            if (p.group_top == 2 && c != 0) v += p.bias ? of_key(c) : score(of_key(c));
         }
         const uint32_t mine = a != 0 ? key_of(v) : 0;
         int rank = 0;
+#pragma unroll 4
         for (int h = 0; h < p.groups; ++h) {
             const uint32_t o = __shfl_sync(kAll, mine, h * p.lanes);
             rank += o > mine || (o == mine && h < g);
@@ -238,50 +334,37 @@ route_kernel(const __grid_constant__ RouteParams p) {
             if (last != 0) {
                 const int at = __ffs(last) - 1;
                 const float edge = __shfl_sync(kAll, v, at);
-                const uint32_t ea = __shfl_sync(kAll, a, at), eb = __shfl_sync(kAll, b, at);
                 const bool close =
-                    there && near(fmaxf(v, edge), fminf(v, edge), 2.f * tol + fabsf(edge) * 0x1p-22f);
-                const bool alike = !p.bias && a == ea && b == eb;
-                if (__any_sync(kAll, close && !keep) && __any_sync(kAll, close && !alike && rank != p.top_groups - 1))
-                    keep = exact_groups(row, key, exact_scores(row, p.sigmoid, most), p, lane);
+                    there && near(fmaxf(v, edge), fminf(v, edge), 4.f * tol + fabsf(edge) * 0x1p-22f);
+                if (__any_sync(kAll, close && !keep)) {
+                    const uint32_t ea = __shfl_sync(kAll, a, at), ec = __shfl_sync(kAll, c, at);
+                    const bool alike = !p.bias && a == ea && c == ec;
+                    if (__any_sync(kAll, close && !alike && rank != p.top_groups - 1))
+                        keep = exact_groups(row, key, exact_scores(row, p.sigmoid, most), p, lane);
+                }
             }
         }
+        if (!keep) {
+            best.key = best.second = 0;
 #pragma unroll
-        for (int i = 0; i < HELD; ++i)
-            if (!keep) key[i] = 0;
+            for (int i = 0; i < HELD; ++i) key[i] = 0;
+        }
     }
 
     // the largest key of the warp, top_k times; lane j keeps the j-th
-    uint32_t best = 0;
-    int best_i = 0;
-    auto rescan = [&] {
-        best = 0;
-#pragma unroll
-        for (int i = HELD - 1; i >= 0; --i)
-            if (key[i] >= best) {
-                best = key[i];
-                best_i = i;
-            }
-    };
-    rescan();
     uint32_t my_key = 0;
     int my_e = -1, n = 0;
     auto take = [&] {
-        const uint32_t top = __reduce_max_sync(kAll, best);
+        const uint32_t top = __reduce_max_sync(kAll, best.key);
         if (top == 0) return false;
-        const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
-        const int e = __shfl_sync(kAll, row.first + best_i, from);
+        const int from = __ffs(__ballot_sync(kAll, best.key == top)) - 1;
+        const int e = __shfl_sync(kAll, row.first + best.at, from);
         if (lane == n) {
             my_key = top;
             my_e = e;
         }
         ++n;
-        if (lane == from) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                if (i == best_i) key[i] = 0;
-            rescan();
-        }
+        if (lane == from) best.take(key);
         return true;
     };
     while (n < p.top_k && take()) {
@@ -292,77 +375,83 @@ route_kernel(const __grid_constant__ RouteParams p) {
         const float my_b = my_e >= 0 ? row.bias_at(my_e) : 0.f;
         const float c = of_key(my_key);
         const float next_c = __shfl_down_sync(kAll, c, 1);
-        const float next_l = __shfl_down_sync(kAll, my_l, 1), next_b = __shfl_down_sync(kAll, my_b, 1);
-        bool unsure = lane + 1 < n && near(c, next_c, 2.f * tol) && !(my_l == next_l && my_b == next_b);
         const float edge = __shfl_sync(kAll, c, n - 1);
-        const float edge_l = __shfl_sync(kAll, my_l, n - 1), edge_b = __shfl_sync(kAll, my_b, n - 1);
-        int close = 0;   // of what is left, as near to the last one chosen
+        const bool tight = lane + 1 < n && near(c, next_c, 2.f * tol);
+        const bool crowd = best.key != 0 && near(edge, of_key(best.key), 2.f * tol);
+        if (__any_sync(kAll, tight || crowd)) {
+            // near, but perhaps of the same logit and bias: then the order is right
+            const float next_l = __shfl_down_sync(kAll, my_l, 1), next_b = __shfl_down_sync(kAll, my_b, 1);
+            const float edge_l = __shfl_sync(kAll, my_l, n - 1), edge_b = __shfl_sync(kAll, my_b, n - 1);
+            bool unsure = tight && !(my_l == next_l && my_b == next_b);
+            int close = 0;   // of what is left, as near to the last one chosen
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            if (key[i] != 0 && near(edge, of_key(key[i]), 2.f * tol)) {
-                ++close;
-                unsure |= !(l[i] == edge_l && row.bias_at(row.first + i) == edge_b);
+            for (int i = 0; i < HELD; ++i) {
+                if (best.taken >> i & 1) key[i] = 0;
+                if (key[i] != 0 && near(edge, of_key(key[i]), 2.f * tol)) {
+                    ++close;
+                    unsure |= !(counted(l[i]) == edge_l && row.bias_at(row.first + i) == edge_b);
+                }
             }
-        }
-        if (__any_sync(kAll, unsure)) {
-            const Exact exact = exact_scores(row, p.sigmoid, most);
-            const int chosen = n, all = chosen + __reduce_add_sync(kAll, close);
-            if (all <= 32) {
-                // a candidate a lane, each at its rank among them
-                while (n < all && take()) {
-                }
-                const double d = my_e >= 0 ? exact(row.logit(my_e), row.bias_at(my_e)) : -INFINITY;
-                int rank = 0;
-                for (int i = 0; i < n; ++i) {
-                    const double o = __shfl_sync(kAll, d, i);
-                    const int oe = __shfl_sync(kAll, my_e, i);
-                    rank += o > d || (o == d && oe < my_e);
-                }
-                int e = -1;
-                for (int i = 0; i < n; ++i) {
-                    const int r = __shfl_sync(kAll, rank, i), oe = __shfl_sync(kAll, my_e, i);
-                    if (r == lane) e = oe;
-                }
-                my_e = lane < chosen ? e : -1;
-            } else {
-                // every expert that is left, by binary64 values, one after another
-                for (int j = 0; j < chosen; ++j) {
-                    const int e = __shfl_sync(kAll, my_e, j);
+            if (__any_sync(kAll, unsure)) {
+                const Exact exact = exact_scores(row, p.sigmoid, most);
+                const int chosen = n, all = chosen + __reduce_add_sync(kAll, close);
+                if (all <= 32) {
+                    // a candidate a lane, each at its rank among them
+                    while (n < all && take()) {
+                    }
+                    const double d = my_e >= 0 ? exact(row.logit(my_e), row.bias_at(my_e)) : -INFINITY;
+                    int rank = 0;
+                    for (int i = 0; i < n; ++i) {
+                        const double o = __shfl_sync(kAll, d, i);
+                        const int oe = __shfl_sync(kAll, my_e, i);
+                        rank += o > d || (o == d && oe < my_e);
+                    }
+                    int e = -1;
+                    for (int i = 0; i < n; ++i) {
+                        const int r = __shfl_sync(kAll, rank, i), oe = __shfl_sync(kAll, my_e, i);
+                        if (r == lane) e = oe;
+                    }
+                    my_e = lane < chosen ? e : -1;
+                } else {
+                    // every expert that is left, by binary64 values, one after another
+                    for (int j = 0; j < chosen; ++j) {
+                        const int e = __shfl_sync(kAll, my_e, j);
 #pragma unroll
-                    for (int i = 0; i < HELD; ++i)
-                        if (i < row.n && row.first + i == e) key[i] = 1;
-                }
-                for (int j = 0; j < chosen; ++j) {
-                    double most_d = -INFINITY;
-                    int at = 0x7fffffff;
+                        for (int i = 0; i < HELD; ++i)
+                            if (i < row.n && row.first + i == e) key[i] = 1;
+                    }
+                    for (int j = 0; j < chosen; ++j) {
+                        double most_d = -INFINITY;
+                        int at = 0x7fffffff;
 #pragma unroll 1
-                    for (int i = 0; i < row.n; ++i) {
-                        bool in = false;
+                        for (int i = 0; i < row.n; ++i) {
+                            bool in = false;
 #pragma unroll
-                        for (int q = 0; q < HELD; ++q) in |= q == i && key[q] != 0;
-                        if (!in) continue;
-                        const double d = exact(row.logit(row.first + i), row.bias_at(row.first + i));
-                        if (at == 0x7fffffff || d > most_d) {
-                            most_d = d;
-                            at = row.first + i;
+                            for (int q = 0; q < HELD; ++q) in |= q == i && key[q] != 0;
+                            if (!in) continue;
+                            const double d = exact(row.logit(row.first + i), row.bias_at(row.first + i));
+                            if (at == 0x7fffffff || d > most_d) {
+                                most_d = d;
+                                at = row.first + i;
+                            }
                         }
-                    }
-                    for (int o = 16; o > 0; o >>= 1) {
-                        const double od = __shfl_xor_sync(kAll, most_d, o);
-                        const int oa = __shfl_xor_sync(kAll, at, o);
-                        if (od > most_d || (od == most_d && oa < at)) {
-                            most_d = od;
-                            at = oa;
+                        for (int o = 16; o > 0; o >>= 1) {
+                            const double od = __shfl_xor_sync(kAll, most_d, o);
+                            const int oa = __shfl_xor_sync(kAll, at, o);
+                            if (od > most_d || (od == most_d && oa < at)) {
+                                most_d = od;
+                                at = oa;
+                            }
                         }
-                    }
-                    if (lane == j) my_e = at;
+                        if (lane == j) my_e = at;
 #pragma unroll
-                    for (int i = 0; i < HELD; ++i)
-                        if (i < row.n && row.first + i == at) key[i] = 0;
+                        for (int i = 0; i < HELD; ++i)
+                            if (i < row.n && row.first + i == at) key[i] = 0;
+                    }
                 }
+                n = chosen;
+                my_l = my_e >= 0 ? row.logit(my_e) : minus_infinity();
             }
-            n = chosen;
-            my_l = my_e >= 0 ? row.logit(my_e) : minus_infinity();
         }
     }
 
@@ -379,7 +468,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
         const float s = warp_sum(w);
         w = s > 0.f ? w / s : 0.f;
     } else if (mine) {
-        w = score(my_l);
+        w = p.sigmoid ? sigmoid_of(my_l) : expf(my_l - most) * inv;
     }
     if (lane < p.top_k) {
         const size_t at = token * p.top_k + lane;
@@ -391,9 +480,9 @@ route_kernel(const __grid_constant__ RouteParams p) {
 // ---------------------------------------------------------------- backward --
 
 // A warp a token: the chosen experts' shares in the lanes, then the row.  Without
-// renormalisation a softmax has a gradient for every expert; else the row is zeros but
-// for the chosen ones.
-template <typename T>
+// renormalisation a softmax has a gradient for every expert, and a lane holds every 32nd
+// of the row (HELD of them); else the row is zeros but for the chosen ones.
+template <typename T, int HELD>
 __global__ void __launch_bounds__(32 * kRouteWarps)
 route_backward_kernel(const __grid_constant__ RouteParams p) {
     const int lane = threadIdx.x & 31;
@@ -401,6 +490,13 @@ route_backward_kernel(const __grid_constant__ RouteParams p) {
     if (token >= p.tokens) return;   // whole warps
     const T *row = static_cast<const T *>(p.logits) + token * p.ld;
     T *out = static_cast<T *>(p.dlogits) + token * p.ldd;
+    const bool dense = !p.sigmoid && !p.renormalise;
+    float d[HELD];
+    if (dense) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            d[i] = lane + 32 * i < p.experts ? counted(value_of(row + lane + 32 * i)) : minus_infinity();
+    }
     int e = -1;
     float l = minus_infinity(), g = 0.f;
     if (lane < p.top_k) {
@@ -414,32 +510,33 @@ route_backward_kernel(const __grid_constant__ RouteParams p) {
         }
     }
     const bool real = e >= 0 && l >= -kMaxFinite;
-    const bool dense = !p.sigmoid && !p.renormalise;
-    float v = 0.f, total = 0.f, most = 0.f, inv = 0.f;
+    float v = 0.f, total = 0.f, share = 0.f;
     if (p.renormalise) {
         const float top = warp_max(real ? l : minus_infinity());
         float n = 0.f;
         if (real)
             n = p.sigmoid ? expf(fminf(l, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(l)))
                           : expf(l - top);
-        const float s = warp_sum(n), share = s > 0.f ? n / s : 0.f;
+        const float s = warp_sum(n);
+        share = s > 0.f ? n / s : 0.f;
         const float mean = warp_sum(real ? g * share : 0.f);
         if (real) v = share * (g - mean) * (p.sigmoid ? sigmoid_of(-l) : 1.f);
     } else if (p.sigmoid) {
         if (real) v = g * sigmoid_of(l) * sigmoid_of(-l);
     } else {
-        most = minus_infinity();
-        for (int i = lane; i < p.experts; i += 32) most = fmaxf(most, counted(value_of(row + i)));
-        most = warp_max(most);
-        float s = 0.f;
-        if (most >= -kMaxFinite)
-            for (int i = lane; i < p.experts; i += 32) s += expf(counted(value_of(row + i)) - most);
+        float most = minus_infinity(), s = 0.f;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) most = fmaxf(most, d[i]);
+        most = fmaxf(warp_max(most), -kMaxFinite);   // (an empty row: exp(-inf) each)
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) s += d[i] = expf(d[i] - most);
         s = warp_sum(s);
-        inv = s == 0.f ? 0.f : 1.f / s;   // (NaN for a row with a NaN)
-        const float share = real ? expf(l - most) * inv : 0.f;
-        total = warp_sum(real ? g * share : 0.f);
+        const float inv = s == 0.f ? 0.f : 1.f / s;   // (NaN for a row with a NaN)
+        share = real ? expf(l - most) * inv : 0.f;
         v = real ? g * share : 0.f;
-        l = share;   // (the score, from here on)
+        total = warp_sum(v);
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) d[i] *= -(inv * total);
     }
     // an expert that occurs twice: its shares' sum, in both of its lanes
     const unsigned alike = __match_any_sync(kAll, e);
@@ -451,12 +548,14 @@ route_backward_kernel(const __grid_constant__ RouteParams p) {
         }
         v = sum;
     }
-    if (dense && real) v -= l * total;
-    __syncwarp();   // dlogits may be logits: every lane has read its chosen one
-    for (int i = lane; i < p.experts; i += 32) {
-        float d = 0.f;
-        if (dense && inv != 0.f) d = -expf(counted(value_of(row + i)) - most) * inv * total;
-        put(out + i, d);
+    v -= share * total;   // (0 but where the row is dense)
+    __syncwarp();         // dlogits may be logits: every lane has read its chosen one
+    if (dense) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (lane + 32 * i < p.experts) put(out + lane + 32 * i, d[i]);
+    } else {
+        for (int i = lane; i < p.experts; i += 32) put(out + i, 0.f);
     }
     __syncwarp();
     if (e >= 0) put(out + e, v);
@@ -489,18 +588,47 @@ RouteParams params(const RouteArgs &a) {
     return p;
 }
 
+template <typename T, int HELD>
+void route_held(const RouteArgs &a, const RouteParams &p) {
+    const unsigned grid = (unsigned)((a.tokens + kRouteWarps - 1) / kRouteWarps);
+    constexpr size_t kBytes = HELD * sizeof(T) < 16 ? HELD * sizeof(T) : 16;
+    constexpr bool kWhole = HELD >= 4 && kBytes == 16;   // (below, scalar loads are as good)
+    if constexpr (kWhole) {
+        if (p.lanes * p.held == p.each && p.held == HELD && p.lanes * p.groups == 32 &&
+            reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ld * sizeof(T) % 16 == 0 &&
+            reinterpret_cast<uintptr_t>(a.bias) % 16 == 0) {
+            route_kernel<T, HELD, true><<<grid, 32 * kRouteWarps, 0, a.stream>>>(p);
+            return;
+        }
+    }
+    route_kernel<T, HELD, false><<<grid, 32 * kRouteWarps, 0, a.stream>>>(p);
+}
+
 template <typename T>
 cudaError_t route_typed(const RouteArgs &a) {
     const RouteParams p = params(a);
+    if (p.held <= 1) route_held<T, 1>(a, p);
+    else if (p.held <= 2) route_held<T, 2>(a, p);
+    else if (p.held <= 4) route_held<T, 4>(a, p);
+    else if (p.held <= 8) route_held<T, 8>(a, p);
+    else if (p.held <= 16) route_held<T, 16>(a, p);
+    else if (p.held <= 32) route_held<T, 32>(a, p);
+    else route_held<T, 64>(a, p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t route_backward_typed(const RouteArgs &a) {
+    const RouteParams p = params(a);
     const unsigned grid = (unsigned)((a.tokens + kRouteWarps - 1) / kRouteWarps);
+    const int held = a.sigmoid || a.renormalise ? 1 : (a.experts + 31) / 32;
     constexpr int kBlock = 32 * kRouteWarps;
-    if (p.held <= 1) route_kernel<T, 1><<<grid, kBlock, 0, a.stream>>>(p);
-    else if (p.held <= 2) route_kernel<T, 2><<<grid, kBlock, 0, a.stream>>>(p);
-    else if (p.held <= 4) route_kernel<T, 4><<<grid, kBlock, 0, a.stream>>>(p);
-    else if (p.held <= 8) route_kernel<T, 8><<<grid, kBlock, 0, a.stream>>>(p);
-    else if (p.held <= 16) route_kernel<T, 16><<<grid, kBlock, 0, a.stream>>>(p);
-    else if (p.held <= 32) route_kernel<T, 32><<<grid, kBlock, 0, a.stream>>>(p);
-    else route_kernel<T, 64><<<grid, kBlock, 0, a.stream>>>(p);
+    if (held <= 1) route_backward_kernel<T, 1><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (held <= 2) route_backward_kernel<T, 2><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (held <= 4) route_backward_kernel<T, 4><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (held <= 8) route_backward_kernel<T, 8><<<grid, kBlock, 0, a.stream>>>(p);
+    else if (held <= 16) route_backward_kernel<T, 16><<<grid, kBlock, 0, a.stream>>>(p);
+    else route_backward_kernel<T, 32><<<grid, kBlock, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -511,11 +639,7 @@ cudaError_t launch_route(const RouteArgs &a) {
 }
 
 cudaError_t launch_route_backward(const RouteArgs &a) {
-    const RouteParams p = params(a);
-    const unsigned grid = (unsigned)((a.tokens + kRouteWarps - 1) / kRouteWarps);
-    if (a.dtype == PURLIN_F32) route_backward_kernel<float><<<grid, 32 * kRouteWarps, 0, a.stream>>>(p);
-    else route_backward_kernel<__nv_bfloat16><<<grid, 32 * kRouteWarps, 0, a.stream>>>(p);
-    return cudaGetLastError();
+    return a.dtype == PURLIN_F32 ? route_backward_typed<float>(a) : route_backward_typed<__nv_bfloat16>(a);
 }
 
 }  // namespace purlin
