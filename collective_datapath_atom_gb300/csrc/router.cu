@@ -17,6 +17,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "layers.h"
 
 namespace purlin {
@@ -37,7 +39,7 @@ struct RouteParams {
     size_t ld, ldd, tokens;
     int experts, top_k, groups, top_groups, group_top;
     int each;    // experts of a group
-    int lanes;   // lanes of a group
+    int lanes, lane_bits;   // lanes of a group, a power of two
     int held;    // experts of a lane
     bool sigmoid, renormalise;
     float scale;
@@ -149,25 +151,22 @@ __device__ __forceinline__ void load_held(float (&v)[HELD], const __nv_bfloat16 
 // A lane's two largest keys and their places; experts that were taken are out of it.
 template <int HELD>
 struct Best {
-    using Mask = uint64_t;
+    using Mask = std::conditional_t<HELD <= 32, uint32_t, uint64_t>;
     uint32_t key = 0, second = 0;
     int at = 0, second_at = 0;
     Mask taken = 0;
+    template <bool FIRST>
     __device__ __forceinline__ void scan(const uint32_t (&keys)[HELD]) {
         key = second = 0;
         at = second_at = 0;
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
-            const uint32_t k = (HELD <= 32 ? (uint32_t)taken >> i : (uint32_t)(taken >> i)) & 1 ? 0 : keys[i];
-            if (k > key) {
-                second = key;
-                second_at = at;
-                key = k;
-                at = i;
-            } else if (k > second) {
-                second = k;
-                second_at = i;
-            }
+            const uint32_t k = !FIRST && (taken >> i & 1) ? 0 : keys[i];
+            const bool most = k > key, more = k > second;
+            second_at = most ? at : more ? i : second_at;
+            second = max(second, min(key, k));
+            at = most ? i : at;
+            key = max(key, k);
         }
     }
     // The largest is taken; a lane that has given two looks for the rest again.
@@ -179,7 +178,7 @@ struct Best {
             second = 0;
             fresh = false;
         } else if (!fresh) {
-            scan(keys);
+            scan<false>(keys);
             fresh = true;
         } else {
             key = 0;
@@ -204,17 +203,18 @@ __device__ __noinline__ Exact exact_scores(const Row<T, HELD> &row, bool sigmoid
     return x;
 }
 
-// Whether this lane's group is kept, by binary64 values.
+// Whether this lane's group is kept, by binary64 values.  `least`: experts of the group
+// with smaller keys are none of its two largest.
 template <typename T, int HELD>
-__device__ __noinline__ bool exact_groups(const Row<T, HELD> &row, const uint32_t (&key)[HELD],
+__device__ __noinline__ bool exact_groups(const Row<T, HELD> &row, const uint32_t (&key)[HELD], uint32_t least,
                                           const Exact &exact, const RouteParams &p, int lane) {
     double a = -INFINITY, b = -INFINITY;   // the lane's two largest
-#pragma unroll 1
-    for (int i = 0; i < row.n; ++i) {
-        bool in = false;
+    uint64_t left = 0;
 #pragma unroll
-        for (int q = 0; q < HELD; ++q) in |= q == i && key[q] != 0;
-        if (!in) continue;
+    for (int i = 0; i < HELD; ++i) left |= (uint64_t)(key[i] != 0 && key[i] >= least) << i;
+    while (left != 0) {
+        const int i = __ffsll(left) - 1;
+        left &= left - 1;
         const double d = exact(row.logit(row.first + i), row.bias_at(row.first + i));
         if (d > a) {
             b = a;
@@ -223,6 +223,7 @@ __device__ __noinline__ bool exact_groups(const Row<T, HELD> &row, const uint32_
             b = d;
         }
     }
+    __syncwarp();
     for (int o = 1; o < p.lanes; o <<= 1) {
         const double oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
         b = fmax(fmin(a, oa), fmax(b, ob));
@@ -245,7 +246,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
     const int lane = threadIdx.x & 31;
     const size_t token = (size_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     if (token >= p.tokens) return;   // whole warps
-    const int g = lane / p.lanes, sub = lane - g * p.lanes;
+    const int g = lane >> p.lane_bits, sub = lane & (p.lanes - 1);
     Row<T, HELD> row;
     row.logits = static_cast<const T *>(p.logits) + token * p.ld;
     row.bias = p.bias;
@@ -273,24 +274,24 @@ route_kernel(const __grid_constant__ RouteParams p) {
     bad = __any_sync(kAll, bad);
     most = counted(warp_max(most));
     float inv = 0.f;   // softmax: 1 / the sum of exp(l - most)
-    const bool whole = !p.sigmoid && most >= -kMaxFinite && (p.bias || !p.renormalise || p.group_top == 2);
-    if (whole) {
-        float s = 0.f;
+    if (!p.sigmoid && most >= -kMaxFinite && (p.bias || !p.renormalise || p.group_top == 2)) {
+        float s = 0.f, e[HELD];
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) s += expf(counted(l[i]) - most);
+        for (int i = 0; i < HELD; ++i) {
+            e[i] = expf(counted(l[i]) - most);
+            s += bad && l[i] != l[i] ? 0.f : e[i];   // (without NaNs the choice is of the rest)
+        }
         inv = 1.f / warp_sum(s);
-        if (bad) {   // (then the choice is of the rest)
-            s = 0.f;
+        if (p.bias) {
 #pragma unroll
-            for (int i = 0; i < HELD; ++i) s += l[i] == l[i] ? expf(counted(l[i]) - most) : 0.f;
-            inv = 1.f / warp_sum(s);
+            for (int i = 0; i < HELD; ++i) l[i] = l[i] >= -kMaxFinite ? e[i] * inv : minus_infinity();
         }
     }
     // an error of the choice values: of the scores, none above the largest one's (l e^-l
     // falls), and of a sum's rounding.  Softmax: the exponential, the quotient and HELD + 5
     // additions
     const float largest = p.sigmoid ? choice_sigmoid(most) : inv;
-    const float tol = largest * (p.sigmoid ? 4.f + 1.2f * fmaxf(-most, 0.f) : (float)(HELD + 16)) * 0x1p-22f + 0x1p-120f;
+    const float tol = largest * (p.sigmoid ? 4.f + 1.2f * fminf(fmaxf(-most, 0.f), 200.f) : (float)(HELD + 16)) * 0x1p-22f + 0x1p-120f;
     auto near = [&](float hi, float lo, float by) {   // not told apart, infinities too
         return !(hi - lo > by + fabsf(hi) * 0x1p-22f);
     };
@@ -298,13 +299,14 @@ route_kernel(const __grid_constant__ RouteParams p) {
     uint32_t key[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-        float c;
-        if (p.bias) c = score(p.sigmoid ? l[i] : counted(l[i])) + b[i];
-        else c = counted(l[i]);
+        float c = l[i];
+        if (!p.bias) c = counted(c);
+        else if (p.sigmoid) c = choice_sigmoid(c) + b[i];
+        else c += b[i];
         key[i] = l[i] >= -kMaxFinite && c > minus_infinity() ? key_of(c) : 0;
     }
     Best<HELD> best;
-    best.scan(key);
+    best.template scan<true>(key);
 
     if (p.top_groups < p.groups) {
         uint32_t a = best.key, c = best.second;   // the group's two largest keys
@@ -339,8 +341,13 @@ route_kernel(const __grid_constant__ RouteParams p) {
                 if (__any_sync(kAll, close && !keep)) {
                     const uint32_t ea = __shfl_sync(kAll, a, at), ec = __shfl_sync(kAll, c, at);
                     const bool alike = !p.bias && a == ea && c == ec;
-                    if (__any_sync(kAll, close && !alike && rank != p.top_groups - 1))
-                        keep = exact_groups(row, key, exact_scores(row, p.sigmoid, most), p, lane);
+                    if (__any_sync(kAll, close && !alike && rank != p.top_groups - 1)) {
+                        const uint32_t edge_key = p.group_top == 2 && c != 0 ? c : a;
+                        const float edge_c = of_key(edge_key);
+                        const float under = edge_c - (2.f * tol + fabsf(edge_c) * 0x1p-22f);
+                        const uint32_t least = !p.bias ? edge_key : under == under ? key_of(under) : 1;
+                        keep = exact_groups(row, key, least, exact_scores(row, p.sigmoid, most), p, lane);
+                    }
                 }
             }
         }
@@ -389,7 +396,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
                 if (best.taken >> i & 1) key[i] = 0;
                 if (key[i] != 0 && near(edge, of_key(key[i]), 2.f * tol)) {
                     ++close;
-                    unsure |= !(counted(l[i]) == edge_l && row.bias_at(row.first + i) == edge_b);
+                    unsure |= !(row.logit(row.first + i) == edge_l && row.bias_at(row.first + i) == edge_b);
                 }
             }
             if (__any_sync(kAll, unsure)) {
@@ -581,6 +588,7 @@ RouteParams params(const RouteArgs &a) {
     int pow2 = 1;
     while (pow2 < a.groups) pow2 *= 2;
     p.lanes = 32 / pow2;
+    while (1 << p.lane_bits < p.lanes) ++p.lane_bits;
     p.held = (p.each + p.lanes - 1) / p.lanes;
     p.sigmoid = a.sigmoid;
     p.renormalise = a.renormalise;
