@@ -226,7 +226,8 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) write_pairs<T, V, EDGE>(total, vectors.column(i), hidden, t[i]);
         }
-        // behind a barrier, the stage is free for another row
+        ring.settle();   // the row before's refill, before a barrier
+        // behind one, the stage is free for another row
         if (!p.y) {
             team.sync();
             ring.refill();
@@ -271,8 +272,10 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
                 }
             }
         }
-        ring.settle();
-        if (EDGE && plan.stages == 1) team.sync();   // the next row's ends are read at once
+        if (EDGE && plan.stages == 1) {   // the next row's ends are read at once
+            ring.settle();
+            team.sync();
+        }
         ring.next();
     }
     if (team.thread == 0) ring.drain();

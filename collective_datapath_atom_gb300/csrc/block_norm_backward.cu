@@ -320,6 +320,7 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
                 nt = fma2(mul2(pair_of(gk[h], j), pair_of(wk, j)), u, nt);
             }
         }
+        ring.settle();   // the row before's refill, before a barrier
         float sx = low(xx) + high(xx), st = low(tt) + high(tt), sn = low(nt) + high(nt);
         team.sums(sx, st, sn, sums[turn][slot]);
         auto refill = [&] {   // behind a barrier: every thread has its share of the row
@@ -390,8 +391,10 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
             }
             write_pairs<T, V, EDGE>(dx, vectors.column(i), hidden, h[i]);
         }
-        ring.settle();
-        if (EDGE && plan.stages == 1) team.sync();   // the next row's ends are read at once
+        if (EDGE && plan.stages == 1) {   // the next row's ends are read at once
+            ring.settle();
+            team.sync();
+        }
         ring.next();
     }
     if (team.thread == 0) ring.drain();

@@ -199,6 +199,7 @@ struct TeamRing {
     size_t next_row, step;
     uint32_t issued = 0;
     bool dead = false;      // a wait expired: no more of them
+    bool pending = false;   // a refill whose ends are still to be put in place
     T end[EDGE ? kEnds : 1];
     int place[EDGE ? kEnds : 1];   // of this thread's ends: elements from the row's start, or -1
 
@@ -237,27 +238,31 @@ struct TeamRing {
     // Every thread, behind a barrier after which the row at hand is no longer read from
     // its stage: the next row is on its way there.
     __device__ __forceinline__ void refill() {
-        if (next_row >= p.rows || dead) return;
-        if (team.thread == 0) issue();
+        pending = next_row < p.rows && !dead;
+        if (pending && team.thread == 0) issue();
         if constexpr (EDGE) {
+            // every thread loads, some element of its block's first row where it has none to:
+            // behind a branch the compiler waits for the load (8000 x 4000 f32 of pitch 4099,
+            // backward, 171 us, so 164; aligned 128)
+            const size_t row = pending ? next_row : blockIdx.x;
 #pragma unroll
             for (int k = 0; k < kEnds; ++k) {
-                if (place[k] < 0) continue;
-                const int a = end_array(k);
-                end[k] = static_cast<const T *>(p.src[a])[next_row * p.ld[a] + place[k]];
+                const int a = min(end_array(k), arrays - 1);
+                end[k] = static_cast<const T *>(p.src[a])[row * p.ld[a] + max(place[k], 0)];
             }
         }
     }
-    // Every thread, later: and its ends are in place, for reads behind the team's next barrier.
+    // Every thread, later: and its ends are in place, for reads behind the team's next
+    // barrier.  Nothing where no refill is pending.
     __device__ __forceinline__ void settle() {
-        if (next_row >= p.rows || dead) return;
+        if (!pending) return;
+        pending = false;
         if constexpr (EDGE) {
 #pragma unroll
-            for (int k = 0; k < kEnds; ++k) {
+            for (int k = 0; k < kEnds; ++k)
                 if (place[k] >= 0)
                     reinterpret_cast<T *>(smem() + base + fill * stage_bytes +
                                           end_array(k) * array_bytes)[phase + place[k]] = end[k];
-            }
         }
         ++issued;
         fill = fill + 1 == stages ? 0 : fill + 1;
@@ -417,7 +422,7 @@ TeamShape team_shape(size_t rows, size_t hidden, bool edge, int arrays, bool wei
     TeamShape s;
     if (rows < (size_t)sms) return s;
     const int warps = (int)(warps_of(windows_of<V>(hidden, edge), items) / 32);
-    if (warps > kTeamWarps || warps > block_warps) return s;
+    if (warps > std::min(kTeamWarps, block_warps)) return s;
     const size_t windows = (size_t)items * warps * 32;
     const size_t stage = windows * 16 * (size_t)arrays, room = kTeamSmem;
     for (int want = 2; want >= 1; --want)
