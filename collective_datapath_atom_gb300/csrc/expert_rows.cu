@@ -40,19 +40,34 @@ struct OrderParams {
     int run;          // slots of a warp, a multiple of 32
 };
 
+// 32 kBatch slots of a warp's run, loaded together: -1 where there is none.
+constexpr int kBatch = 8;
+
+__device__ __forceinline__ void load_slots(const OrderParams &p, size_t from, int left, int (&e)[kBatch]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const size_t s = from + 32 * k + lane;
+        const int v = 32 * k < left && s < p.slots ? p.chosen[s] : -1;
+        e[k] = (unsigned)v < (unsigned)p.groups ? v : -1;
+    }
+}
+
 // Counts of this warp's run into its row of `hist`, which is zero.
 __device__ __forceinline__ void count_run(const OrderParams &p, int *hist) {
-    const int lane = threadIdx.x & 31;
     const size_t from = ((size_t)blockIdx.x * kOrderWarps + (threadIdx.x >> 5)) * p.run;
-    for (int i = 0; i < p.run; i += 32) {
-        const size_t s = from + i + lane;
-        const int e = s < p.slots ? p.chosen[s] : -1;
-        if ((unsigned)e < (unsigned)p.groups) atomicAdd(&hist[e], 1);
+    for (int i = 0; i < p.run; i += 32 * kBatch) {
+        int e[kBatch];
+        load_slots(p, from + i, p.run - i, e);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (e[k] >= 0) atomicAdd(&hist[e[k]], 1);
     }
 }
 
 __global__ void __launch_bounds__(kOrderThreads)
 order_count_kernel(const __grid_constant__ OrderParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the places may be launched
     extern __shared__ int hist[];
     for (int e = threadIdx.x; e < p.groups; e += kOrderThreads) hist[e] = 0;
     __syncthreads();
@@ -62,39 +77,59 @@ order_count_kernel(const __grid_constant__ OrderParams p) {
         p.partial[(size_t)blockIdx.x * p.groups + e] = hist[e];
 }
 
-// Shared memory: kOrderWarps x groups counts, then groups totals.
-__global__ void __launch_bounds__(kOrderThreads)
+// Shared memory: kOrderWarps x groups counts, then totals and counts of the blocks before.
+// The first kOrderWarps warps have slots; where there are many blocks, as many more help
+// to add up their counts, eight loads at once (64 blocks of 256 threads, a thread an
+// expert, took 14 us over it).
+constexpr int kPlaceThreads = 1024, kAtOnce = 8;
+
+__global__ void __launch_bounds__(kPlaceThreads)
 order_place_kernel(const __grid_constant__ OrderParams p) {
     extern __shared__ int hist[];
     __shared__ long long warp_total[kOrderWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = p.groups;
-    int *total = hist + kOrderWarps * groups;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = p.groups, threads = (int)blockDim.x;
+    int *total = hist + kOrderWarps * groups, *earlier = total + groups;
     int *own = hist + warp * groups;
-    for (int e = threadIdx.x; e < kOrderWarps * groups; e += kOrderThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < (kOrderWarps + 2) * groups; e += threads) hist[e] = 0;
     __syncthreads();
-    count_run(p, own);
-    __syncthreads();
-    // the run's counts become the slots of the expert before it; of other blocks by their totals
-    for (int e = threadIdx.x; e < groups; e += kOrderThreads) {
-        int before = 0, sum = 0;
-        if (gridDim.x > 1) {
-            for (unsigned b = 0; b < gridDim.x; ++b) {
-                const int c = p.partial[(size_t)b * groups + e];
-                if (b < blockIdx.x) before += c;
-                sum += c;
+    if (warp < kOrderWarps) count_run(p, own);
+    // launched while the other blocks' counts are still being taken: wait for all of them
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (gridDim.x > 1) {
+        const int blocks = (int)gridDim.x, pieces = (blocks + kAtOnce - 1) / kAtOnce;
+        for (int i = threadIdx.x; i < groups * pieces; i += threads) {
+            const int piece = i / groups, e = i - piece * groups;
+            int c[kAtOnce], before = 0, sum = 0;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int b = min(piece * kAtOnce + k, blocks - 1);
+                c[k] = p.partial[(size_t)b * groups + e];
             }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int b = piece * kAtOnce + k;
+                sum += b < blocks ? c[k] : 0;
+                before += b < (int)blockIdx.x ? c[k] : 0;
+            }
+            atomicAdd(&total[e], sum);   // (whole numbers: in any order)
+            atomicAdd(&earlier[e], before);
         }
+    }
+    __syncthreads();
+    // the run's counts become the slots of the expert before it
+    for (int e = threadIdx.x; e < groups; e += threads) {
+        int before = earlier[e];
         for (int w = 0; w < kOrderWarps; ++w) {
             const int c = hist[w * groups + e];
             hist[w * groups + e] = before;
             before += c;
         }
-        total[e] = gridDim.x > 1 ? sum : before;
+        if (gridDim.x == 1) total[e] = before;
     }
     __syncthreads();
     // the experts' first rows: capacities, or the totals before, a piece of them a thread
     const int each = (groups + kOrderThreads - 1) / kOrderThreads;
-    const int first = threadIdx.x * each, last = min(groups, first + each);
+    const int first = min(groups, (int)threadIdx.x * each), last = min(groups, first + each);
     long long sum = 0;
     for (int e = first; e < last; ++e) sum += total[e];
     long long scan = sum;
@@ -103,10 +138,10 @@ order_place_kernel(const __grid_constant__ OrderParams p) {
         const long long v = __shfl_up_sync(kAll, scan, o);
         if (lane >= o) scan += v;
     }
-    if (lane == 31) warp_total[warp] = scan;
+    if (lane == 31 && warp < kOrderWarps) warp_total[warp] = scan;
     __syncthreads();
     long long at = scan - sum;
-    for (int w = 0; w < warp; ++w) at += warp_total[w];
+    for (int w = 0; w < min(warp, kOrderWarps); ++w) at += warp_total[w];
     for (int e = first; e < last; ++e) {
         const int n = total[e];
         const long long row = p.capacity ? (long long)e * (long long)p.capacity : at;
@@ -118,18 +153,24 @@ order_place_kernel(const __grid_constant__ OrderParams p) {
         at += n;
     }
     __syncthreads();
+    if (warp >= kOrderWarps) return;
     const size_t from = ((size_t)blockIdx.x * kOrderWarps + warp) * p.run;
-    for (int i = 0; i < p.run; i += 32) {
-        const size_t s = from + i + lane;
-        const int e = s < p.slots ? p.chosen[s] : -1;
-        const bool in = (unsigned)e < (unsigned)groups;
-        const unsigned alike = __match_any_sync(kAll, in ? e : -1);
-        const int rank = in ? own[e] + __popc(alike & ((1u << lane) - 1)) : 0;
-        __syncwarp();
-        if (in && (alike >> lane) == 1) own[e] = rank + 1;   // the last lane of its expert
-        __syncwarp();
-        if (s < p.slots)
-            p.place[s] = in && (p.capacity == 0 || rank < (long long)p.capacity) ? total[e] + rank : -1;
+    for (int i = 0; i < p.run; i += 32 * kBatch) {
+        int e[kBatch];
+        unsigned alike[kBatch];
+        load_slots(p, from + i, p.run - i, e);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) alike[k] = __match_any_sync(kAll, e[k]);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int rank = e[k] >= 0 ? own[e[k]] + __popc(alike[k] & ((1u << lane) - 1)) : 0;
+            __syncwarp();
+            if (e[k] >= 0 && (alike[k] >> lane) == 1) own[e[k]] = rank + 1;   // the last lane of its expert
+            __syncwarp();
+            const size_t s = from + i + 32 * k + lane;
+            if (i + 32 * k < p.run && s < p.slots)
+                p.place[s] = e[k] >= 0 && (p.capacity == 0 || rank < (long long)p.capacity) ? total[e[k]] + rank : -1;
+        }
     }
 }
 
@@ -170,20 +211,30 @@ __device__ __forceinline__ bool inside(int place, size_t rows) {
     return place >= 0 && (size_t)place < rows;
 }
 
-template <int W>
+// EACH accesses a thread, a block apart; a place's share of the row is stored at once,
+// place after place, so that the stores of a block run along a row.
+template <int W, int EACH>
 __global__ void dispatch_kernel(const __grid_constant__ RowsParams p) {
     using A = typename Access<W>::type;
     const size_t token = blockIdx.x / p.parts;
     const uint32_t part = blockIdx.x - (uint32_t)token * p.parts;
-    const uint32_t i = part * blockDim.x + threadIdx.x;
+    const uint32_t first = part * blockDim.x * EACH + threadIdx.x;
     const int32_t *place = p.place + token * p.top_k;
     if (p.scales && part == 0 && threadIdx.x < p.top_k && inside(place[threadIdx.x], p.n_rows))
         p.out_scales[place[threadIdx.x]] = p.scales[token];
-    if (i >= p.accesses) return;
-    const A v = reinterpret_cast<const A *>(p.x + token * p.ldx)[i];
-    for (int j = 0; j < p.top_k; ++j)
-        if (inside(place[j], p.n_rows))
-            reinterpret_cast<A *>(p.out + (size_t)place[j] * p.ldo)[i] = v;
+    A v[EACH];
+#pragma unroll
+    for (int u = 0; u < EACH; ++u)
+        if (first + u * blockDim.x < p.accesses)
+            v[u] = reinterpret_cast<const A *>(p.x + token * p.ldx)[first + u * blockDim.x];
+    for (int j = 0; j < p.top_k; ++j) {
+        const int to = place[j];
+        if (!inside(to, p.n_rows)) continue;
+        A *out = reinterpret_cast<A *>(p.out + (size_t)to * p.ldo);
+#pragma unroll
+        for (int u = 0; u < EACH; ++u)
+            if (first + u * blockDim.x < p.accesses) out[first + u * blockDim.x] = v[u];
+    }
 }
 
 // The N values of type T in an access.
@@ -319,12 +370,12 @@ RowsParams params(const RowsArgs &a, size_t es) {
     return p;
 }
 
-// A thread an access: the blocks of a token, and their threads.
-void spread(RowsParams &p, size_t tokens, unsigned *grid, unsigned *block) {
-    const uint32_t most = 256;
+// `each` accesses a thread: the blocks of a token, and their threads.
+void spread(RowsParams &p, size_t tokens, uint32_t each, unsigned *grid, unsigned *block) {
+    const uint32_t most = 256 * each;
     p.parts = (int)((p.accesses + most - 1) / most);
     if ((size_t)p.parts * tokens > 0x7FFFFFFFu) p.parts = 0;   // (more bytes than the GPU has)
-    *block = p.parts ? ((p.accesses + p.parts - 1) / p.parts + 31) / 32 * 32 : 0;
+    *block = p.parts ? ((p.accesses + p.parts * each - 1) / (p.parts * each) + 31) / 32 * 32 : 0;
     *grid = (unsigned)((size_t)p.parts * tokens);
 }
 
@@ -349,7 +400,7 @@ cudaError_t combine_typed(const RowsArgs &a) {
         constexpr int W = decltype(w)::value;
         p.accesses = (uint32_t)(a.cols * sizeof(T) / W);
         unsigned grid, block;
-        spread(p, a.tokens, &grid, &block);
+        spread(p, a.tokens, 1, &grid, &block);
         if (grid == 0) return cudaErrorInvalidConfiguration;
         combine_kernel<T, W><<<grid, block, 0, a.stream>>>(p);
         return cudaGetLastError();
@@ -380,14 +431,24 @@ cudaError_t launch_expert_order(const OrderArgs &a) {
     const size_t runs = (size_t)blocks * kOrderWarps;
     const size_t run = ((a.slots + runs - 1) / runs + 31) / 32 * 32;
     const OrderParams p{a.chosen, a.place, a.begin, a.count, a.partial, a.slots, a.capacity, a.groups, (int)run};
-    const int smem = (kOrderWarps + 1) * a.groups * (int)sizeof(int);   // 36 KiB at most
+    const int smem = (kOrderWarps + 2) * a.groups * (int)sizeof(int);   // 40 KiB at most
     if (blocks > 1) {
         order_count_kernel<<<blocks, kOrderThreads, a.groups * sizeof(int), a.stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    order_place_kernel<<<blocks, kOrderThreads, smem, a.stream>>>(p);
-    return cudaGetLastError();
+    // its launch overlaps the counts' kernel, which every kernel before it precedes
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)blocks);
+    c.blockDim = dim3(blocks > 1 ? kPlaceThreads : kOrderThreads);
+    c.dynamicSmemBytes = (size_t)smem;
+    c.stream = a.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = blocks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&c, order_place_kernel, p);
 }
 
 cudaError_t launch_dispatch_rows(const RowsArgs &a) {
@@ -397,9 +458,11 @@ cudaError_t launch_dispatch_rows(const RowsArgs &a) {
         constexpr int W = decltype(w)::value;
         p.accesses = (uint32_t)(row_bytes / W);
         unsigned grid, block;
-        spread(p, a.tokens, &grid, &block);
+        const bool many = a.tokens * p.accesses >= (size_t)a.sms * 8192;
+        spread(p, a.tokens, many ? 4 : 1, &grid, &block);
         if (grid == 0) return cudaErrorInvalidConfiguration;
-        dispatch_kernel<W><<<grid, block, 0, a.stream>>>(p);
+        if (many) dispatch_kernel<W, 4><<<grid, block, 0, a.stream>>>(p);
+        else dispatch_kernel<W, 1><<<grid, block, 0, a.stream>>>(p);
         return cudaGetLastError();
     });
 }
