@@ -8,14 +8,14 @@
 // of one expert rank themselves by a match over the warp.  Integers alone: the same
 // places every time.
 //
-// The rows' kernels are bound by bytes.  A thread has one access of a token's row (16
-// bytes where pointers, pitches and columns allow, else the largest power of two that
-// they do) and all of the token's places: dispatch loads once and stores top_k times,
-// combine has top_k loads in flight and adds them up in their order in binary32.
+// The rows' kernels are bound by bytes.  A thread has windows of 16 bytes of a token's
+// row and all of the token's places: dispatch loads once and stores top_k times, combine
+// has several rows' loads in flight and adds them up in their order in binary32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layers.h"
 
@@ -181,136 +181,226 @@ int order_blocks(const OrderArgs &a) {
 
 // -------------------------------------------------------------------- rows --
 
-// An access of W bytes.
+// Rows are read and written in windows of W bytes, 16, 8 or 4, the most that pointers,
+// pitches and columns allow.  W 0, where that is less (bf16 of an odd number of columns,
+// odd bytes): windows of 16 bytes on the boundaries of the row that is written; a row that
+// is read is put in step from two loads, whose second another thread's first brought into
+// the cache.  At a row's ends they bring bytes of the rows beside it, which go nowhere; at
+// the matrix's own ends windows are read element by element, and at a row's written word
+// by word and byte by byte.
 template <int W>
-struct Access;
-template <>
-struct Access<16> { using type = uint4; };
-template <>
-struct Access<8> { using type = uint2; };
-template <>
-struct Access<4> { using type = uint32_t; };
-template <>
-struct Access<2> { using type = uint16_t; };
-template <>
-struct Access<1> { using type = uint8_t; };
+struct Words {
+    uint32_t w[W ? W / 4 : 4];
+};
 
 struct RowsParams {
     const char *x, *rows, *shared;
+    const char *x_end, *rows_end, *shared_end;   // of the matrices
     const float *scales, *weights;
     const int32_t *place;
     char *out;
     float *out_scales;
     size_t ldx, ldr, lds, ldo;   // bytes
-    size_t n_rows;
-    int top_k, parts;            // parts: blocks of a token
-    uint32_t accesses;           // of a row
+    size_t n_rows, tokens;
+    int top_k, parts;            // parts: blocks of a token (backward: places of a block)
+    int64_t row_bytes;
+    uint32_t windows;            // of a row, at the worst place
 };
 
 __device__ __forceinline__ bool inside(int place, size_t rows) {
     return place >= 0 && (size_t)place < rows;
 }
 
-// EACH accesses a thread, a block apart; a place's share of the row is stored at once,
-// place after place, so that the stores of a block run along a row.
-template <int W, int EACH>
-__global__ void dispatch_kernel(const __grid_constant__ RowsParams p) {
-    using A = typename Access<W>::type;
-    const size_t token = blockIdx.x / p.parts;
-    const uint32_t part = blockIdx.x - (uint32_t)token * p.parts;
-    const uint32_t first = part * blockDim.x * EACH + threadIdx.x;
-    const int32_t *place = p.place + token * p.top_k;
-    if (p.scales && part == 0 && threadIdx.x < p.top_k && inside(place[threadIdx.x], p.n_rows))
-        p.out_scales[place[threadIdx.x]] = p.scales[token];
-    A v[EACH];
+// Bytes from a row's start to its window i, on the boundaries of `row`.
+template <int W>
+__device__ __forceinline__ int64_t window_at(const char *row, uint32_t i) {
+    if constexpr (W == 0) return (int64_t)i * 16 - (int64_t)(reinterpret_cast<uintptr_t>(row) & 15);
+    return (int64_t)i * W;
+}
+
+template <int W>
+__device__ __forceinline__ Words<W> load_words(const char *p) {
+    Words<W> v;
+    if constexpr (W == 16 || W == 0) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+    } else if constexpr (W == 8) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        v.w[0] = u.x, v.w[1] = u.y;
+    } else {
+        v.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+    return v;
+}
+
+// A window of a row from `at` on; ES bytes an element.  W 0: of a matrix from `base` to
+// `end`; what lies outside the row is not said.
+template <int W, int ES>
+__device__ __forceinline__ Words<W> read_window(const char *row, int64_t at, int64_t bytes, const char *base,
+                                                const char *end) {
+    if constexpr (W != 0) {
+        return load_words<W>(row + at);
+    } else {
+        const int off = (int)(reinterpret_cast<uintptr_t>(row + at) & 15);
+        const char *p = row + at - off;
+        uint32_t w[8] = {};
+        if (p >= base && p + 32 <= end) {
+            const Words<W> a = load_words<W>(p), b = load_words<W>(p + 16);
 #pragma unroll
-    for (int u = 0; u < EACH; ++u)
-        if (first + u * blockDim.x < p.accesses)
-            v[u] = reinterpret_cast<const A *>(p.x + token * p.ldx)[first + u * blockDim.x];
-    for (int j = 0; j < p.top_k; ++j) {
-        const int to = place[j];
-        if (!inside(to, p.n_rows)) continue;
-        A *out = reinterpret_cast<A *>(p.out + (size_t)to * p.ldo);
+            for (int i = 0; i < 4; ++i) {
+                w[i] = a.w[i];
+                w[i + 4] = b.w[i];
+            }
 #pragma unroll
-        for (int u = 0; u < EACH; ++u)
-            if (first + u * blockDim.x < p.accesses) out[first + u * blockDim.x] = v[u];
+            for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (off & 3) * 8);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16 / ES; ++j) {
+                const int64_t e = at + j * ES;
+                if (e < 0 || e >= bytes) continue;
+                uint32_t v;
+                if constexpr (ES == 2) v = *reinterpret_cast<const uint16_t *>(row + e);
+                else v = *reinterpret_cast<const uint8_t *>(row + e);
+                w[j * ES / 4] |= v << (j * ES % 4 * 8);
+            }
+        }
+        return Words<W>{{w[0], w[1], w[2], w[3]}};
     }
 }
 
-// The N values of type T in an access.
-template <typename T, int N>
-struct Values {
-    T v[N];
-};
-
-template <typename T>
-__device__ __forceinline__ float as_float(T v);
-template <>
-__device__ __forceinline__ float as_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T rounded(float v);
-template <>
-__device__ __forceinline__ float rounded<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-template <typename T, int W>
-__device__ __forceinline__ void load(float (&f)[W / sizeof(T)], const char *row, uint32_t i) {
-    using A = typename Access<W>::type;
-    union {
-        A a;
-        T v[W / sizeof(T)];
-    } u;
-    u.a = reinterpret_cast<const A *>(row)[i];
+template <int W, int ES>
+__device__ __forceinline__ void write_window(char *row, int64_t at, int64_t bytes, const Words<W> &v) {
+    if constexpr (W == 8) {
+        *reinterpret_cast<uint2 *>(row + at) = make_uint2(v.w[0], v.w[1]);
+    } else if constexpr (W == 4) {
+        *reinterpret_cast<uint32_t *>(row + at) = v.w[0];
+    } else if (W == 16 || (at >= 0 && at + 16 <= bytes)) {
+        *reinterpret_cast<uint4 *>(row + at) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    } else if constexpr (W == 0) {
 #pragma unroll
-    for (int q = 0; q < W / (int)sizeof(T); ++q) f[q] = as_float<T>(u.v[q]);
-}
-template <typename T, int W>
-__device__ __forceinline__ void store(char *row, uint32_t i, const float (&f)[W / sizeof(T)]) {
-    using A = typename Access<W>::type;
-    union {
-        A a;
-        T v[W / sizeof(T)];
-    } u;
+        for (int q = 0; q < 4; ++q) {
+            const int64_t word = at + 4 * q;
+            if (word >= 0 && word + 4 <= bytes) {
+                *reinterpret_cast<uint32_t *>(row + word) = v.w[q];
+                continue;
+            }
 #pragma unroll
-    for (int q = 0; q < W / (int)sizeof(T); ++q) u.v[q] = rounded<T>(f[q]);
-    reinterpret_cast<A *>(row)[i] = u.a;
+            for (int j = 0; j < 4 / ES; ++j) {
+                const int64_t e = word + j * ES;
+                if (e < 0 || e >= bytes) continue;
+                if constexpr (ES == 2) *reinterpret_cast<uint16_t *>(row + e) = (uint16_t)(v.w[q] >> (16 * j));
+                else *reinterpret_cast<uint8_t *>(row + e) = (uint8_t)(v.w[q] >> (8 * j));
+            }
+        }
+    }
 }
 
+// blockDim.y tokens a block, or `parts` blocks a token; EACH windows a thread, a block
+// apart.  A place's share of the row is stored at once, place after place, so that the
+// stores of a block run along a row.  In step, x is loaded once for all of the places.
+template <int W, int ES, int EACH>
+__global__ void dispatch_kernel(const __grid_constant__ RowsParams p) {
+    const uint32_t unit = blockIdx.x / p.parts, part = blockIdx.x - unit * p.parts;
+    const size_t token = (size_t)unit * blockDim.y + threadIdx.y;
+    if (token >= p.tokens) return;
+    const uint32_t first = part * blockDim.x * EACH + threadIdx.x;
+    const int32_t *place = p.place + token * p.top_k;
+    const char *x = p.x + token * p.ldx;
+    if (p.scales && part == 0)
+        for (int j = threadIdx.x; j < p.top_k; j += (int)blockDim.x)
+            if (inside(place[j], p.n_rows)) p.out_scales[place[j]] = p.scales[token];
+    Words<W> v[EACH];
+    if constexpr (W != 0) {
+#pragma unroll
+        for (int u = 0; u < EACH; ++u)
+            if (first + u * blockDim.x < p.windows)
+                v[u] = read_window<W, ES>(x, window_at<W>(x, first + u * blockDim.x), p.row_bytes, p.x, p.x_end);
+    }
+    for (int j = 0; j < p.top_k; ++j) {
+        const int to = place[j];
+        if (!inside(to, p.n_rows)) continue;
+        char *out = p.out + (size_t)to * p.ldo;
+        if constexpr (W == 0) {
+#pragma unroll
+            for (int u = 0; u < EACH; ++u)
+                v[u] = read_window<W, ES>(x, window_at<W>(out, first + u * blockDim.x), p.row_bytes, p.x, p.x_end);
+        }
+#pragma unroll
+        for (int u = 0; u < EACH; ++u)
+            if (first + u * blockDim.x < p.windows)
+                write_window<W, ES>(out, window_at<W>(out, first + u * blockDim.x), p.row_bytes, v[u]);
+    }
+}
+
+// A window's values.
+template <typename T, int W>
+__device__ __forceinline__ void unpack(const Words<W> &u, float *f) {
+#pragma unroll
+    for (int q = 0; q < (int)(sizeof(u.w) / 4); ++q) {
+        if constexpr (sizeof(T) == 4) {
+            f[q] = __uint_as_float(u.w[q]);
+        } else {
+            f[2 * q] = __uint_as_float(u.w[q] << 16);
+            f[2 * q + 1] = __uint_as_float(u.w[q] & 0xFFFF0000u);
+        }
+    }
+}
+template <typename T, int W>
+__device__ __forceinline__ Words<W> pack(const float *f) {
+    Words<W> u;
+#pragma unroll
+    for (int q = 0; q < (int)(sizeof(u.w) / 4); ++q) {
+        if constexpr (sizeof(T) == 4) {
+            u.w[q] = __float_as_uint(f[q]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+            u.w[q] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+    return u;
+}
+
+// A thread a window of y; tokens and blocks as above.  (Loads of four rows at a time, ahead
+// of their sums, are slower: 16384 x 7168 bf16 of eight places 434 us, so 348.)
 template <typename T, int W>
 __global__ void combine_kernel(const __grid_constant__ RowsParams p) {
-    constexpr int N = W / sizeof(T);
-    const size_t token = blockIdx.x / p.parts;
-    const uint32_t part = blockIdx.x - (uint32_t)token * p.parts;
+    constexpr int ES = sizeof(T), N = sizeof(Words<W>) / ES;
+    const uint32_t unit = blockIdx.x / p.parts, part = blockIdx.x - unit * p.parts;
+    const size_t token = (size_t)unit * blockDim.y + threadIdx.y;
     const uint32_t i = part * blockDim.x + threadIdx.x;
-    if (i >= p.accesses) return;
+    if (token >= p.tokens || i >= p.windows) return;
+    char *out = p.out + token * p.ldo;
+    const int64_t at = window_at<W>(out, i);
     float sum[N] = {};
-    if (p.shared) load<T, W>(sum, p.shared + token * p.lds, i);
+    if (p.shared) unpack<T>(read_window<W, ES>(p.shared + token * p.lds, at, p.row_bytes, p.shared, p.shared_end), sum);
     for (int j = 0; j < p.top_k; ++j) {
         const int place = p.place[token * p.top_k + j];
         if (!inside(place, p.n_rows)) continue;
         const float w = p.weights ? p.weights[token * p.top_k + j] : 1.f;
-        float v[N];
-        load<T, W>(v, p.rows + (size_t)place * p.ldr, i);
+        float f[N];
+        unpack<T>(read_window<W, ES>(p.rows + (size_t)place * p.ldr, at, p.row_bytes, p.rows, p.rows_end), f);
 #pragma unroll
-        for (int q = 0; q < N; ++q) sum[q] = fmaf(w, v[q], sum[q]);
+        for (int q = 0; q < N; ++q) sum[q] = fmaf(w, f[q], sum[q]);
     }
-    store<T, W>(p.out + token * p.ldo, i, sum);
+    write_window<W, ES>(out, at, p.row_bytes, pack<T, W>(sum));
 }
 
-// A block a token: for each of its places the row's gradient and the product with dy.
+// For a place: the row's gradient and the product with dy.  A block has a token, which
+// reads dy once, or a place where there are too few tokens for the SMs (64 tokens of eight
+// places x 4096 bf16 5.8 us, a block a token 10.5); `parts` places a block.
 template <typename T, int W>
 __global__ void combine_backward_kernel(const __grid_constant__ RowsParams p) {
-    constexpr int N = W / sizeof(T);
+    constexpr int ES = sizeof(T), N = sizeof(Words<W>) / ES;
     __shared__ float sums[2][32];   // places that are there take turns
     int turn = 0;
-    const size_t token = blockIdx.x;
-    const char *dy = p.x + token * p.ldx;
     const int warps = blockDim.x >> 5;
-    for (int j = 0; j < p.top_k; ++j) {
-        const size_t slot = token * p.top_k + j;
+    for (int j = 0; j < p.parts; ++j) {
+        const size_t slot = (size_t)blockIdx.x * p.parts + j;
+        const char *dy = p.x + slot / p.top_k * p.ldx;
         const int place = p.place[slot];
         if (!inside(place, p.n_rows)) {
             if (threadIdx.x == 0) p.out_scales[slot] = 0.f;
@@ -318,17 +408,24 @@ __global__ void combine_backward_kernel(const __grid_constant__ RowsParams p) {
         }
         const float w = p.weights[slot];
         const char *row = p.rows + (size_t)place * p.ldr;
+        char *out = p.out + (size_t)place * p.ldo;
         float dot = 0.f;
-        for (uint32_t i = threadIdx.x; i < p.accesses; i += blockDim.x) {
+        for (uint32_t i = threadIdx.x; i < p.windows; i += blockDim.x) {
+            const int64_t at = window_at<W>(out, i);
             float d[N], v[N];
-            load<T, W>(d, dy, i);
-            load<T, W>(v, row, i);
+            unpack<T>(read_window<W, ES>(dy, at, p.row_bytes, p.x, p.x_end), d);
+            unpack<T>(read_window<W, ES>(row, at, p.row_bytes, p.rows, p.rows_end), v);
+            if (W == 0 && (at < 0 || at + 16 > p.row_bytes)) {
+#pragma unroll
+                for (int q = 0; q < N; ++q)
+                    if (at + q * ES < 0 || at + q * ES >= p.row_bytes) d[q] = v[q] = 0.f;
+            }
 #pragma unroll
             for (int q = 0; q < N; ++q) {
                 dot = fmaf(d[q], v[q], dot);
                 d[q] *= w;
             }
-            store<T, W>(p.out + (size_t)place * p.ldo, i, d);
+            write_window<W, ES>(out, at, p.row_bytes, pack<T, W>(d));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
@@ -342,79 +439,98 @@ __global__ void combine_backward_kernel(const __grid_constant__ RowsParams p) {
     }
 }
 
-// The largest access that the rows of every operand allow.
-int width_of(const RowsParams &p, size_t row_bytes) {
-    size_t all = 16 | row_bytes;
-    for (const void *q : {(const void *)p.x, (const void *)p.rows, (const void *)p.shared, (const void *)p.out})
-        all |= reinterpret_cast<uintptr_t>(q);
-    for (size_t ld : {p.ldx, p.ldr, p.lds, p.ldo}) all |= ld;
-    return (int)(all & (~all + 1));
+// A launch's parameters; the windows' bytes, 0: out of step.
+int params(const RowsArgs &a, size_t es, RowsParams *p) {
+    *p = RowsParams{};
+    p->x = static_cast<const char *>(a.x);
+    p->rows = static_cast<const char *>(a.rows);
+    p->shared = static_cast<const char *>(a.shared);
+    p->scales = a.scales;
+    p->weights = a.weights;
+    p->place = a.place;
+    p->out = static_cast<char *>(a.out);
+    p->out_scales = a.out_scales;
+    p->ldx = a.x ? a.ldx * es : 0;
+    p->ldr = a.rows ? a.ldr * es : 0;
+    p->lds = a.shared ? a.lds * es : 0;
+    p->ldo = a.ldo * es;
+    p->n_rows = a.n_rows;
+    p->tokens = a.tokens;
+    p->top_k = a.top_k;
+    const size_t bytes = a.cols * es;
+    p->x_end = p->x + (a.tokens - 1) * p->ldx + bytes;
+    p->shared_end = p->shared + (a.tokens - 1) * p->lds + bytes;
+    p->rows_end = p->rows + (a.n_rows ? a.n_rows - 1 : 0) * p->ldr + bytes;
+    size_t all = 16 | bytes | p->ldx | p->ldr | p->lds | p->ldo;
+    for (const void *q : {a.x, a.rows, a.shared, (const void *)a.out}) all |= reinterpret_cast<uintptr_t>(q);
+    const int most = (int)(all & (~all + 1)), width = most >= 4 ? most : 0;
+    p->row_bytes = (int64_t)bytes;
+    p->windows = (uint32_t)(width ? bytes / width : (bytes + 30) / 16);
+    return width;
 }
 
-RowsParams params(const RowsArgs &a, size_t es) {
-    RowsParams p{};
-    p.x = static_cast<const char *>(a.x);
-    p.rows = static_cast<const char *>(a.rows);
-    p.shared = static_cast<const char *>(a.shared);
-    p.scales = a.scales;
-    p.weights = a.weights;
-    p.place = a.place;
-    p.out = static_cast<char *>(a.out);
-    p.out_scales = a.out_scales;
-    p.ldx = a.x ? a.ldx * es : 0;
-    p.ldr = a.rows ? a.ldr * es : 0;
-    p.lds = a.shared ? a.lds * es : 0;
-    p.ldo = a.ldo * es;
-    p.n_rows = a.n_rows;
-    p.top_k = a.top_k;
-    return p;
-}
-
-// `each` accesses a thread: the blocks of a token, and their threads.
-void spread(RowsParams &p, size_t tokens, uint32_t each, unsigned *grid, unsigned *block) {
+// `each` windows a thread: the tokens of a block, or the blocks of a token.
+bool spread(RowsParams &p, uint32_t each, unsigned *grid, dim3 *block) {
     const uint32_t most = 256 * each;
-    p.parts = (int)((p.accesses + most - 1) / most);
-    if ((size_t)p.parts * tokens > 0x7FFFFFFFu) p.parts = 0;   // (more bytes than the GPU has)
-    *block = p.parts ? ((p.accesses + p.parts * each - 1) / (p.parts * each) + 31) / 32 * 32 : 0;
-    *grid = (unsigned)((size_t)p.parts * tokens);
+    p.parts = (int)((p.windows + most - 1) / most);
+    uint32_t x = (p.windows + p.parts * each - 1) / (p.parts * each);
+    if (x > 16) {
+        x = (x + 31) / 32 * 32;
+    } else {   // parts of a warp
+        uint32_t pow2 = 1;
+        while (pow2 < x) pow2 *= 2;
+        x = pow2;
+    }
+    *block = dim3(x, 256 / x);
+    const size_t units = (p.tokens + block->y - 1) / block->y;
+    *grid = (unsigned)(units * p.parts);
+    return units * p.parts <= 0x7FFFFFFFu;   // (else they have more bytes than the GPU)
 }
 
-size_t size_of(int dtype) { return dtype == PURLIN_F32 ? 4 : dtype == PURLIN_BF16 ? 2 : 1; }
-
-template <typename T, typename F>
+template <int ES, typename F>
 cudaError_t by_width(int width, F run) {
-    if (width >= 16) return run(std::integral_constant<int, 16>());
+    if (width == 16) return run(std::integral_constant<int, 16>());
     if (width == 8) return run(std::integral_constant<int, 8>());
-    if constexpr (sizeof(T) <= 4)
-        if (width == 4) return run(std::integral_constant<int, 4>());
-    if constexpr (sizeof(T) <= 2)
-        if (width == 2) return run(std::integral_constant<int, 2>());
-    if constexpr (sizeof(T) == 1) return run(std::integral_constant<int, 1>());
-    return cudaErrorInvalidValue;
+    if (width == 4) return run(std::integral_constant<int, 4>());
+    if constexpr (ES < 4) return run(std::integral_constant<int, 0>());
+    return cudaErrorInvalidValue;   // (f32 has 4 bytes at least)
+}
+
+template <int ES>
+cudaError_t dispatch_typed(const RowsArgs &a) {
+    RowsParams p;
+    return by_width<ES>(params(a, ES, &p), [&](auto width) {
+        constexpr int W = decltype(width)::value;
+        const bool many = a.tokens * p.windows >= (size_t)a.sms * 8192 && p.windows >= 256;
+        unsigned grid;
+        dim3 block;
+        if (!spread(p, many ? 4 : 1, &grid, &block)) return cudaErrorInvalidConfiguration;
+        if (many) dispatch_kernel<W, ES, 4><<<grid, block, 0, a.stream>>>(p);
+        else dispatch_kernel<W, ES, 1><<<grid, block, 0, a.stream>>>(p);
+        return cudaGetLastError();
+    });
 }
 
 template <typename T>
 cudaError_t combine_typed(const RowsArgs &a) {
-    RowsParams p = params(a, sizeof(T));
-    return by_width<T>(width_of(p, a.cols * sizeof(T)), [&](auto w) {
-        constexpr int W = decltype(w)::value;
-        p.accesses = (uint32_t)(a.cols * sizeof(T) / W);
-        unsigned grid, block;
-        spread(p, a.tokens, 1, &grid, &block);
-        if (grid == 0) return cudaErrorInvalidConfiguration;
-        combine_kernel<T, W><<<grid, block, 0, a.stream>>>(p);
+    RowsParams p;
+    return by_width<sizeof(T)>(params(a, sizeof(T), &p), [&](auto width) {
+        unsigned grid;
+        dim3 block;
+        if (!spread(p, 1, &grid, &block)) return cudaErrorInvalidConfiguration;
+        combine_kernel<T, decltype(width)::value><<<grid, block, 0, a.stream>>>(p);
         return cudaGetLastError();
     });
 }
 
 template <typename T>
 cudaError_t combine_backward_typed(const RowsArgs &a) {
-    RowsParams p = params(a, sizeof(T));
-    return by_width<T>(width_of(p, a.cols * sizeof(T)), [&](auto w) {
-        constexpr int W = decltype(w)::value;
-        p.accesses = (uint32_t)(a.cols * sizeof(T) / W);
-        const unsigned block = std::min(256u, std::max(32u, (p.accesses + 31) / 32 * 32));
-        combine_backward_kernel<T, W><<<(unsigned)a.tokens, block, 0, a.stream>>>(p);
+    RowsParams p;
+    return by_width<sizeof(T)>(params(a, sizeof(T), &p), [&](auto width) {
+        p.parts = a.tokens < 4 * (size_t)a.sms ? 1 : a.top_k;
+        const unsigned grid = (unsigned)(a.tokens * a.top_k / p.parts);
+        const unsigned block = std::min(256u, std::max(32u, (p.windows + 31) / 32 * 32));
+        combine_backward_kernel<T, decltype(width)::value><<<grid, block, 0, a.stream>>>(p);
         return cudaGetLastError();
     });
 }
@@ -452,19 +568,9 @@ cudaError_t launch_expert_order(const OrderArgs &a) {
 }
 
 cudaError_t launch_dispatch_rows(const RowsArgs &a) {
-    RowsParams p = params(a, size_of(a.dtype));
-    const size_t row_bytes = a.cols * size_of(a.dtype);
-    return by_width<char>(width_of(p, row_bytes), [&](auto w) {
-        constexpr int W = decltype(w)::value;
-        p.accesses = (uint32_t)(row_bytes / W);
-        unsigned grid, block;
-        const bool many = a.tokens * p.accesses >= (size_t)a.sms * 8192;
-        spread(p, a.tokens, many ? 4 : 1, &grid, &block);
-        if (grid == 0) return cudaErrorInvalidConfiguration;
-        if (many) dispatch_kernel<W, 4><<<grid, block, 0, a.stream>>>(p);
-        else dispatch_kernel<W, 1><<<grid, block, 0, a.stream>>>(p);
-        return cudaGetLastError();
-    });
+    return a.dtype == PURLIN_F32    ? dispatch_typed<4>(a)
+           : a.dtype == PURLIN_BF16 ? dispatch_typed<2>(a)
+                                    : dispatch_typed<1>(a);
 }
 
 cudaError_t launch_combine_rows(const RowsArgs &a) {
