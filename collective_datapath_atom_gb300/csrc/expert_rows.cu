@@ -182,12 +182,17 @@ int order_blocks(const OrderArgs &a) {
 // -------------------------------------------------------------------- rows --
 
 // Rows are read and written in windows of W bytes, 16, 8 or 4, the most that pointers,
-// pitches and columns allow.  W 0, where that is less (bf16 of an odd number of columns,
-// odd bytes): windows of 16 bytes on the boundaries of the row that is written; a row that
-// is read is put in step from two loads, whose second another thread's first brought into
-// the cache.  At a row's ends they bring bytes of the rows beside it, which go nowhere; at
-// the matrix's own ends windows are read element by element, and at a row's written word
-// by word and byte by byte.
+// pitches and columns allow.  W 0, where that is too little: windows of 16 bytes on the
+// boundaries of the row that is written; a row that is read is put in step from two loads,
+// whose second another thread's first brought into the cache.  At a row's ends they bring
+// bytes of the rows beside it, which go nowhere; at the matrix's own ends windows are read
+// element by element, and at a row's written word by word and byte by byte.
+// What is too little was measured, 16384 tokens of eight places: windows of 4 bytes lose in
+// combine (2050 bf16 162 us, out of step 134; 1021 f32 150 and 129) and in copies of bf16
+// and f32 (8000 x 4098 135 and 121), and win in copies of bytes (1020 50 and 81) and in the
+// backward pass, which has two rows to put in step (2050 bf16 355 and 477); windows of 8
+// win or are level.  Element by element bf16 of 1021 columns took 134 us (now 75), backward
+// 290 (239).
 template <int W>
 struct Words {
     uint32_t w[W ? W / 4 : 4];
@@ -263,7 +268,8 @@ __device__ __forceinline__ Words<W> read_window(const char *row, int64_t at, int
                 const int64_t e = at + j * ES;
                 if (e < 0 || e >= bytes) continue;
                 uint32_t v;
-                if constexpr (ES == 2) v = *reinterpret_cast<const uint16_t *>(row + e);
+                if constexpr (ES == 4) v = *reinterpret_cast<const uint32_t *>(row + e);
+                else if constexpr (ES == 2) v = *reinterpret_cast<const uint16_t *>(row + e);
                 else v = *reinterpret_cast<const uint8_t *>(row + e);
                 w[j * ES / 4] |= v << (j * ES % 4 * 8);
             }
@@ -288,6 +294,7 @@ __device__ __forceinline__ void write_window(char *row, int64_t at, int64_t byte
                 *reinterpret_cast<uint32_t *>(row + word) = v.w[q];
                 continue;
             }
+            if constexpr (ES == 4) continue;
 #pragma unroll
             for (int j = 0; j < 4 / ES; ++j) {
                 const int64_t e = word + j * ES;
@@ -439,8 +446,8 @@ __global__ void combine_backward_kernel(const __grid_constant__ RowsParams p) {
     }
 }
 
-// A launch's parameters; the windows' bytes, 0: out of step.
-int params(const RowsArgs &a, size_t es, RowsParams *p) {
+// A launch's parameters; the windows' bytes, 0 where they would be fewer than `least`.
+int params(const RowsArgs &a, size_t es, int least, RowsParams *p) {
     *p = RowsParams{};
     p->x = static_cast<const char *>(a.x);
     p->rows = static_cast<const char *>(a.rows);
@@ -463,7 +470,7 @@ int params(const RowsArgs &a, size_t es, RowsParams *p) {
     p->rows_end = p->rows + (a.n_rows ? a.n_rows - 1 : 0) * p->ldr + bytes;
     size_t all = 16 | bytes | p->ldx | p->ldr | p->lds | p->ldo;
     for (const void *q : {a.x, a.rows, a.shared, (const void *)a.out}) all |= reinterpret_cast<uintptr_t>(q);
-    const int most = (int)(all & (~all + 1)), width = most >= 4 ? most : 0;
+    const int most = (int)(all & (~all + 1)), width = most >= least ? most : 0;
     p->row_bytes = (int64_t)bytes;
     p->windows = (uint32_t)(width ? bytes / width : (bytes + 30) / 16);
     return width;
@@ -487,19 +494,21 @@ bool spread(RowsParams &p, uint32_t each, unsigned *grid, dim3 *block) {
     return units * p.parts <= 0x7FFFFFFFu;   // (else they have more bytes than the GPU)
 }
 
-template <int ES, typename F>
+template <int ES, int LEAST, typename F>
 cudaError_t by_width(int width, F run) {
     if (width == 16) return run(std::integral_constant<int, 16>());
     if (width == 8) return run(std::integral_constant<int, 8>());
-    if (width == 4) return run(std::integral_constant<int, 4>());
-    if constexpr (ES < 4) return run(std::integral_constant<int, 0>());
-    return cudaErrorInvalidValue;   // (f32 has 4 bytes at least)
+    if constexpr (LEAST <= 4)
+        if (width == 4) return run(std::integral_constant<int, 4>());
+    if constexpr (LEAST > ES) return run(std::integral_constant<int, 0>());
+    return cudaErrorInvalidValue;
 }
 
 template <int ES>
 cudaError_t dispatch_typed(const RowsArgs &a) {
+    constexpr int kLeast = ES == 1 ? 4 : 8;
     RowsParams p;
-    return by_width<ES>(params(a, ES, &p), [&](auto width) {
+    return by_width<ES, kLeast>(params(a, ES, kLeast, &p), [&](auto width) {
         constexpr int W = decltype(width)::value;
         const bool many = a.tokens * p.windows >= (size_t)a.sms * 8192 && p.windows >= 256;
         unsigned grid;
@@ -514,7 +523,7 @@ cudaError_t dispatch_typed(const RowsArgs &a) {
 template <typename T>
 cudaError_t combine_typed(const RowsArgs &a) {
     RowsParams p;
-    return by_width<sizeof(T)>(params(a, sizeof(T), &p), [&](auto width) {
+    return by_width<sizeof(T), 8>(params(a, sizeof(T), 8, &p), [&](auto width) {
         unsigned grid;
         dim3 block;
         if (!spread(p, 1, &grid, &block)) return cudaErrorInvalidConfiguration;
@@ -526,7 +535,7 @@ cudaError_t combine_typed(const RowsArgs &a) {
 template <typename T>
 cudaError_t combine_backward_typed(const RowsArgs &a) {
     RowsParams p;
-    return by_width<sizeof(T)>(params(a, sizeof(T), &p), [&](auto width) {
+    return by_width<sizeof(T), 4>(params(a, sizeof(T), 4, &p), [&](auto width) {
         p.parts = a.tokens < 4 * (size_t)a.sms ? 1 : a.top_k;
         const unsigned grid = (unsigned)(a.tokens * a.top_k / p.parts);
         const unsigned block = std::min(256u, std::max(32u, (p.windows + 31) / 32 * 32));
