@@ -12,7 +12,8 @@ ctypes binding, so this module only marshals arguments.
     finalize(h)
 
 The layer operators that follow the collectives take one rank's tensors:
-``rms_norm``, ``grouped_matmul`` and their gradients.  They run on the handle's
+``rms_norm``, ``block_norm``, ``route``, ``expert_order``, ``dispatch_rows``,
+``combine_rows``, ``grouped_matmul`` and their gradients.  They run on the handle's
 stream (or on ``stream``), and so do the allocation and the zeroing of results
 that are not passed in.  Where that is not torch's current stream, order the two
 as for any stream's results: the inputs before the call, the results after it.
@@ -22,12 +23,16 @@ from __future__ import annotations
 import enum
 from typing import Sequence
 
-from . import (PURLIN_BF16, PURLIN_E4M3, PURLIN_F32, PURLIN_WEIGHTS_KN, PURLIN_WEIGHTS_NK, Context,
+from . import (PURLIN_BF16, PURLIN_E4M3, PURLIN_F32, PURLIN_GATE_COLUMNS, PURLIN_GATE_ROWS,
+               PURLIN_SIGMOID, PURLIN_SOFTMAX, PURLIN_WEIGHTS_KN, PURLIN_WEIGHTS_NK, Context,
                _stream_handle, purlin_all_gather, purlin_all_gather_v, purlin_all_reduce,
-               purlin_all_to_all, purlin_all_to_all_v, purlin_check, purlin_finalize,
-               purlin_grouped_matmul, purlin_grouped_matmul_weight_grad, purlin_init,
-               purlin_reduce_scatter, purlin_reduce_scatter_v, purlin_rms_norm,
-               purlin_rms_norm_backward, purlin_set_stream)
+               purlin_all_to_all, purlin_all_to_all_v, purlin_block_norm,
+               purlin_block_norm_backward, purlin_check, purlin_combine_rows,
+               purlin_combine_rows_backward, purlin_dispatch_rows, purlin_expert_order,
+               purlin_finalize, purlin_grouped_matmul, purlin_grouped_matmul_weight_grad,
+               purlin_init, purlin_reduce_scatter, purlin_reduce_scatter_v, purlin_rms_norm,
+               purlin_rms_norm_backward, purlin_route, purlin_route_backward, purlin_router,
+               purlin_set_stream)
 
 
 class ReductionMode(enum.Enum):
@@ -284,6 +289,246 @@ def rms_norm_backward(dy, total, weight, handle, dtotal=None, dx=None, dweight=N
     purlin_rms_norm_backward(handle, dy, total, weight, dx, dweight, rows, hidden, eps, d,
                              dtotal=dtotal, lddy=lddy, ldt=ldt, lddt=lddt, lddx=lddx)
     return dx, dweight
+
+
+def _gate(gate, like):
+    """(layout, row stride) of a gate: a value a column, or one an element."""
+    if gate is None:
+        return PURLIN_GATE_COLUMNS, 0
+    if gate.dim() == 1:
+        _vector("gate", gate, like.shape[1], like.dtype)
+        return PURLIN_GATE_COLUMNS, 0
+    return PURLIN_GATE_ROWS, _same_rows("gate", gate, like)
+
+
+def block_norm(x, weight, handle, residual=None, post_weight=None, gate=None, residual_scale=1.0,
+               block_scale=1.0, out=None, total=None, scales=None, eps=1e-5, quantize=False,
+               stream=None):
+    """Norm of ``t = residual_scale * residual + block_scale * gate * u`` times
+    ``weight``, where ``u`` is the block's output ``x``, or its norm times
+    ``post_weight``.  ``gate``: a value a column, or as many as ``x`` has.  Returns
+    ``(out, total)``, or ``(out, total, scales)`` with ``quantize`` (e4m3 rows, a
+    float32 scale a row); ``total`` is ``t``.  ``weight`` None: only ``total``, and
+    ``out`` is None.  Outputs are allocated unless passed in."""
+    import torch
+
+    rows, hidden, ldx = _rows("x", x, (torch.float32, torch.bfloat16))
+    d = PURLIN_F32 if x.dtype == torch.float32 else PURLIN_BF16
+    for name, v in (("weight", weight), ("post_weight", post_weight)):
+        if v is not None:
+            _vector(name, v, hidden, x.dtype)
+    layout, ldg = _gate(gate, x)
+    ldr = _same_rows("residual", residual, x) if residual is not None else 0
+    if weight is None and (quantize or out is not None):
+        raise ValueError("without a weight there is no norm to write")
+    total = _new(handle, stream, x.device, (rows, hidden), x.dtype) if total is None else total
+    ldt = _same_rows("total", total, x)
+    kind = torch.float8_e4m3fn if quantize else x.dtype
+    ldy = 0
+    if weight is not None:
+        if out is None:
+            out = _new(handle, stream, x.device, (rows, hidden), kind)
+        if out.shape != x.shape:
+            raise ValueError("out has the shape of x")
+        ldy = _rows("out", out, (kind,))[2]
+    if quantize and scales is None:
+        scales = _new(handle, stream, x.device, (rows,), torch.float32)
+    if scales is not None:
+        if not quantize:
+            raise ValueError("scales belong to a quantized output")
+        _vector("scales", scales, rows, torch.float32)
+    _on(handle, stream)
+    purlin_block_norm(handle, x, weight, out, rows, hidden, eps, d, PURLIN_E4M3 if quantize else d,
+                      residual=residual, post_weight=post_weight, gate=gate, gate_layout=layout,
+                      residual_scale=residual_scale, block_scale=block_scale, total=total,
+                      scales=scales, ldx=ldx, ldg=ldg, ldr=ldr, ldy=ldy, ldt=ldt)
+    return (out, total, scales) if quantize else (out, total)
+
+
+def block_norm_backward(dy, x, total, weight, handle, dtotal=None, post_weight=None, gate=None,
+                        residual_scale=1.0, block_scale=1.0, eps=1e-5, stream=None):
+    """Gradients of :func:`block_norm` at ``x`` and ``total``: a dict of ``dx``,
+    ``dresidual``, and those of ``dweight``, ``dpost_weight`` and ``dgate`` whose
+    inputs are given (vectors in float32).  ``dtotal``: the gradient that reaches
+    ``total`` from elsewhere.  ``dy``, ``total`` and ``weight`` None: the forward
+    pass wrote ``total`` alone."""
+    import torch
+
+    rows, hidden, ldx = _rows("x", x, (torch.float32, torch.bfloat16))
+    d = PURLIN_F32 if x.dtype == torch.float32 else PURLIN_BF16
+    for name, v in (("weight", weight), ("post_weight", post_weight)):
+        if v is not None:
+            _vector(name, v, hidden, x.dtype)
+    layout, ldg = _gate(gate, x)
+    ld = {name: _same_rows(name, t, x) if t is not None else 0
+          for name, t in (("dy", dy), ("total", total), ("dtotal", dtotal))}
+
+    def new(shape, dtype):
+        return _new(handle, stream, x.device, shape, dtype)
+
+    got = {"dx": new((rows, hidden), x.dtype), "dresidual": new((rows, hidden), x.dtype)}
+    if weight is not None:
+        got["dweight"] = new((hidden,), torch.float32)
+    if post_weight is not None:
+        got["dpost_weight"] = new((hidden,), torch.float32)
+    if gate is not None:
+        got["dgate"] = new((rows, hidden), x.dtype) if layout == PURLIN_GATE_ROWS else \
+            new((hidden,), torch.float32)
+    _on(handle, stream)
+    purlin_block_norm_backward(handle, dy, x, total, weight, got["dx"], got.get("dweight"), rows,
+                               hidden, eps, d, dtotal=dtotal, post_weight=post_weight, gate=gate,
+                               gate_layout=layout, residual_scale=residual_scale,
+                               block_scale=block_scale, dresidual=got["dresidual"],
+                               dpost_weight=got.get("dpost_weight"), dgate=got.get("dgate"),
+                               lddy=ld["dy"], lddt=ld["dtotal"], ldx=ldx, ldt=ld["total"], ldg=ldg)
+    return got
+
+
+def router(experts, top_k, scores="softmax", groups=1, top_groups=1, group_top=1,
+           renormalise=False, scale=1.0):
+    """How :func:`route` chooses: see ``purlin_router`` in include/purlin.h."""
+    kinds = {"softmax": PURLIN_SOFTMAX, "sigmoid": PURLIN_SIGMOID}
+    if scores not in kinds:
+        raise ValueError(f"scores are 'softmax' or 'sigmoid', got {scores!r}")
+    if scale == 0:
+        raise ValueError("a scale of 0 would read as 1")
+    return purlin_router(experts=experts, top_k=top_k, scores=kinds[scores], groups=groups,
+                         top_groups=top_groups, group_top=group_top, renormalise=int(renormalise),
+                         scale=scale)
+
+
+def route(logits, config, handle, bias=None, stream=None):
+    """Each token's experts (int32, falling) and their weights (float32), both
+    tokens x top_k, from its row of ``logits``; ``config`` is a :func:`router`.
+    Returns ``(weights, experts)``; an expert of -1 is none."""
+    import torch
+
+    tokens, _, ld = _rows("logits", logits, (torch.float32, torch.bfloat16), config.experts)
+    d = PURLIN_F32 if logits.dtype == torch.float32 else PURLIN_BF16
+    if bias is not None:
+        _vector("bias", bias, config.experts, torch.float32)
+    weights = _new(handle, stream, logits.device, (tokens, config.top_k), torch.float32)
+    chosen = _new(handle, stream, logits.device, (tokens, config.top_k), torch.int32)
+    _on(handle, stream)
+    purlin_route(handle, logits, weights, chosen, tokens, config, d, bias=bias, ld=ld)
+    return weights, chosen
+
+
+def _slots(name, t, tokens, top_k, dtype):
+    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != (tokens, top_k):
+        raise ValueError(f"{name} must be {tokens} x {top_k} contiguous values on the GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+
+
+def route_backward(dweights, logits, experts, config, handle, stream=None):
+    """Gradient of :func:`route`'s weights with respect to ``logits``."""
+    import torch
+
+    tokens, cols, ld = _rows("logits", logits, (torch.float32, torch.bfloat16), config.experts)
+    d = PURLIN_F32 if logits.dtype == torch.float32 else PURLIN_BF16
+    _slots("dweights", dweights, tokens, config.top_k, torch.float32)
+    _slots("experts", experts, tokens, config.top_k, torch.int32)
+    out = _new(handle, stream, logits.device, (tokens, cols), logits.dtype)
+    _on(handle, stream)
+    purlin_route_backward(handle, dweights, logits, experts, out, tokens, config, d, ld=ld)
+    return out
+
+
+def expert_order(experts, groups, handle, capacity=0, stream=None):
+    """The row of each slot of ``experts`` (int32, as :func:`route` gives them) in
+    the order of the experts, packed or in buffers of ``capacity`` rows (-1 past
+    it).  Returns ``(place, begin, count)``: int32 in the shape of ``experts``, and
+    int64 first rows and counts as :func:`grouped_matmul` takes them."""
+    import torch
+
+    if not experts.is_cuda or not experts.is_contiguous():
+        raise ValueError("experts must be contiguous values on the GPU")
+    if experts.dtype != torch.int32:
+        raise TypeError(f"experts: {experts.dtype}, expected {torch.int32}")
+    place = _new(handle, stream, experts.device, tuple(experts.shape), torch.int32)
+    begin = _new(handle, stream, experts.device, (groups,), torch.int64)
+    count = _new(handle, stream, experts.device, (groups,), torch.int64)
+    _on(handle, stream)
+    purlin_expert_order(handle, experts, place, begin, count, int(experts.numel()), groups,
+                        capacity)
+    return place, begin, count
+
+
+def dispatch_rows(x, place, handle, out_rows=None, scales=None, out=None, out_scales=None,
+                  stream=None):
+    """``out[place[t, j]] = x[t]`` (and its scale) for every token and choice.
+    ``out_rows``: rows of ``out``, as many as slots unless given.  Rows that no place
+    names are left as they are (zero where ``out`` is allocated here).  Returns
+    ``out``, or ``(out, out_scales)`` with ``scales``."""
+    import torch
+
+    kinds = {torch.float32: PURLIN_F32, torch.bfloat16: PURLIN_BF16,
+             torch.float8_e4m3fn: PURLIN_E4M3}
+    tokens, cols, ldx = _rows("x", x, tuple(kinds))
+    top_k = place.shape[-1]
+    _slots("place", place, tokens, top_k, torch.int32)
+    if out is None:
+        rows = tokens * top_k if out_rows is None else out_rows
+        out = _new(handle, stream, x.device, (rows, cols), torch.uint8 if x.dtype ==
+                   torch.float8_e4m3fn else x.dtype, zero=True)
+        out = out.view(x.dtype)
+    rows, _, ldo = _rows("out", out, (x.dtype,), cols)
+    if out_rows is not None and rows != out_rows:
+        raise ValueError(f"out has {rows} rows, expected {out_rows}")
+    if scales is not None:
+        _vector("scales", scales, tokens, torch.float32)
+        if out_scales is None:
+            out_scales = _new(handle, stream, x.device, (rows,), torch.float32, zero=True)
+        _vector("out_scales", out_scales, rows, torch.float32)
+    elif out_scales is not None:
+        raise ValueError("out_scales are copies of scales")
+    _on(handle, stream)
+    purlin_dispatch_rows(handle, x, place, out, tokens, top_k, cols, rows, kinds[x.dtype],
+                         scales=scales, out_scales=out_scales, ldx=ldx, ldo=ldo)
+    return out if scales is None else (out, out_scales)
+
+
+def combine_rows(rows, place, handle, weights=None, shared=None, out=None, stream=None):
+    """For each token the sum of ``weights[t, j] * rows[place[t, j]]`` (on
+    ``shared[t]``, if given); with ``weights`` None the gradient of
+    :func:`dispatch_rows`' ``x`` from that of its output."""
+    import torch
+
+    n_rows, cols, ldr = _rows("rows", rows, (torch.float32, torch.bfloat16))
+    d = PURLIN_F32 if rows.dtype == torch.float32 else PURLIN_BF16
+    tokens, top_k = place.shape
+    _slots("place", place, tokens, top_k, torch.int32)
+    if weights is not None:
+        _slots("weights", weights, tokens, top_k, torch.float32)
+    out = _new(handle, stream, rows.device, (tokens, cols), rows.dtype) if out is None else out
+    out_rows, _, ldy = _rows("out", out, (rows.dtype,), cols)
+    if out_rows != tokens:
+        raise ValueError(f"out has {out_rows} rows, expected {tokens}")
+    lds = _same_rows("shared", shared, out) if shared is not None else 0
+    _on(handle, stream)
+    purlin_combine_rows(handle, rows, place, out, tokens, top_k, cols, n_rows, d, weights=weights,
+                        shared=shared, ldr=ldr, lds=lds, ldy=ldy)
+    return out
+
+
+def combine_rows_backward(dy, rows, place, weights, handle, stream=None):
+    """Gradients of :func:`combine_rows`: ``(drows, dweights)``.  Rows of drows that
+    no place names are zero."""
+    import torch
+
+    n_rows, cols, ldr = _rows("rows", rows, (torch.float32, torch.bfloat16))
+    d = PURLIN_F32 if rows.dtype == torch.float32 else PURLIN_BF16
+    tokens, _, lddy = _rows("dy", dy, (rows.dtype,), cols)
+    top_k = place.shape[-1]
+    _slots("place", place, tokens, top_k, torch.int32)
+    _slots("weights", weights, tokens, top_k, torch.float32)
+    drows = _new(handle, stream, rows.device, (n_rows, cols), rows.dtype, zero=True)
+    dweights = _new(handle, stream, rows.device, (tokens, top_k), torch.float32)
+    _on(handle, stream)
+    purlin_combine_rows_backward(handle, dy, rows, place, weights, drows, dweights, tokens, top_k,
+                                 cols, n_rows, d, lddy=lddy, ldr=ldr)
+    return drows, dweights
 
 
 def _stack(name, t, dtypes):
