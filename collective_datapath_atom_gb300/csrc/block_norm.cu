@@ -182,6 +182,8 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
     constexpr int kResidual = GATES ? 2 : 1;
     const int slot = team.warps == 1 ? 0 : team.index;
     for (int i = threadIdx.x; i < (int)(sizeof(sums) / sizeof(float)); i += (int)blockDim.x) (&sums[0][0][0][0])[i] = 0.f;
+    ring.clear();
+    team.sync();
     ring.start();
     vectors.start();
     __syncthreads();

@@ -290,6 +290,8 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         (&sums[0][0][0][0])[i] = 0.f;
         if (i < (int)(sizeof(last) / sizeof(float))) (&last[0][0][0])[i] = 0.f;
     }
+    ring.clear();
+    team.sync();
     ring.start();
     vectors.start();
     __syncthreads();

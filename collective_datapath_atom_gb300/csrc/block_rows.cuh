@@ -268,8 +268,8 @@ struct TeamRing {
         fill = fill + 1 == stages ? 0 : fill + 1;
         next_row += step;
     }
-    // Every thread, once: zeros, barriers, and the first rows.  A block barrier follows.
-    __device__ void start() {
+    // Every thread, once: zeros and barriers.  A barrier of the team follows.
+    __device__ void clear() {
         if constexpr (EDGE) {
 #pragma unroll
             for (int k = 0; k < kEnds; ++k) place[k] = end_place(k);
@@ -283,7 +283,9 @@ struct TeamRing {
             for (int i = 0; i < stages; ++i) atom::mbar_init(&full[i], 1);
             atom::mbar_init_fence();
         }
-        team.sync();
+    }
+    // Every thread, behind it: the first rows.  A block barrier follows.
+    __device__ void start() {
         for (int i = 0; i < stages; ++i) {
             refill();
             settle();
