@@ -157,7 +157,7 @@ block_norm_kernel(const __grid_constant__ BlockParams p) {
 // A thread holds ITEMS windows of its row's t, made behind the first sum's barrier from
 // operands that it reads from the stage again.  Holding those, which frees the stage a
 // barrier earlier, needs 128 registers, and three teams of seven warps are worth more
-// than early loads: TEAMS3.
+// than early loads (16384 x 7168 bf16 to e4m3 140 us, two teams that hold them 153).
 constexpr int kForwardWarps = 21;
 
 // Operands of the rows, in the order of their arrays in a stage: x, the gates where

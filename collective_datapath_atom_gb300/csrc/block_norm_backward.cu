@@ -11,7 +11,13 @@
 namespace purlin {
 namespace {
 
-constexpr int kBackwardWarps = 16;         // of a block of teams
+// Warps of a block of teams, with two windows a thread; or fewer, with four and with all
+// the registers there are, so that what is done once a row and thread is half as much
+// (32768 x 4096 bf16 266 us, else 281; 16384 x 7168 265 and 295; 8000 x 4096 f32 132 and
+// 136). That needs rows of four warps or more (20000 x 2048, two of them, 122 and 111),
+// teams that leave one warp idle at most (8000 x 2560 f32, three idle, 122 and 95) and
+// rows enough for its slower first and last ones (2000 x 4096 37 and 35, 500 rows 21 and 19).
+constexpr int kBackwardWarps = 16, kFewWarps = 8;
 constexpr size_t kDirectThreadsSm = 512;   // rows on the registers: threads an SM
 
 struct BlockBackwardParams {
@@ -270,11 +276,11 @@ struct TeamParams : BlockBackwardParams {
     size_t ld[5];
 };
 
-template <typename T, int V, int ITEMS, bool EDGE, bool GATES, bool HOLD>
-__global__ void __launch_bounds__(32 * kBackwardWarps)
+template <typename T, int V, int ITEMS, bool EDGE, bool GATES, bool HOLD, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
 block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __grid_constant__ TeamPlan plan) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
-    __shared__ uint64_t full[kBackwardWarps][kMaxStages];
+    __shared__ uint64_t full[WARPS][kMaxStages];
     // rows take turns
     __shared__ __align__(16) float sums[2][kTeams][3][kTeamWarps], last[2][kTeams][kTeamWarps];
     const Team team(plan.warps);
@@ -480,6 +486,7 @@ bool wants_sums(const BlockNormBackwardArgs &a) {
 struct BlockBackwardShape : Shape {
     TeamShape team;   // plan.warps 0: none
     int team_items = 0;
+    bool few_warps = false;
     bool windows = false, edge = false, wide = false;
 };
 
@@ -506,6 +513,15 @@ BlockBackwardShape block_backward_shape(const BlockNormBackwardArgs &a) {
     if (s.windows && a.weight) {
         const int arrays = 3 + (a.dtotal ? 1 : 0) + (gates ? 1 : 0);
         const bool factors = a.post_weight || (a.gate && !a.gate_rows);
+        const int warps = (int)(warps_of(windows_of<V>(a.hidden, s.edge), 4) / 32);
+        s.few_warps = warps >= 4 && warps <= kFewWarps && kFewWarps % warps <= 1 && a.rows / a.sms >= 32;
+        if (s.few_warps) {
+            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, 4, true, kFewWarps,
+                                   kFewWarps, a.sms);
+            s.grid = s.team.grid;
+            if (s.team.plan.warps != 0) return s;
+        }
+        s.few_warps = false;
         for (s.team_items = 2; s.team_items <= 32 / V; s.team_items *= 2) {
             s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, s.team_items, true, kBackwardWarps,
                                    kBackwardWarps, a.sms);
@@ -532,14 +548,14 @@ BlockBackwardShape block_backward_shape(const BlockNormBackwardArgs &a) {
     return s;
 }
 
-template <typename T, int V, int ITEMS, bool EDGE, bool GATES>
+template <typename T, int V, int ITEMS, bool EDGE, bool GATES, int WARPS = kBackwardWarps>
 cudaError_t backward_teams(const BlockNormBackwardArgs &a, const TeamParams &p, const TeamShape &s) {
-    constexpr bool HOLD = ITEMS == 2;
+    constexpr bool HOLD = ITEMS == 2 || WARPS != kBackwardWarps;
     static SharedMemoryLimit limit;
-    const cudaError_t ready =
-        limit.raise(block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD>, kTeamSmem);
+    const auto kernel = block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD, WARPS>;
+    const cudaError_t ready = limit.raise(kernel, kTeamSmem);
     if (ready != cudaSuccess) return ready;
-    block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD><<<s.grid, s.threads, s.smem, a.stream>>>(p, s.plan);
+    kernel<<<s.grid, s.threads, s.smem, a.stream>>>(p, s.plan);
     return cudaGetLastError();
 }
 
@@ -548,6 +564,7 @@ cudaError_t backward_teams(const BlockNormBackwardArgs &a, const BlockBackwardPa
                            const BlockBackwardShape &s) {
     const TeamParams p{b, {a.x, a.dy, a.total, GATES ? a.gate : a.dtotal, a.dtotal},
                        {a.ldx, a.lddy, a.ldt, GATES ? a.ldg : a.lddt, a.lddt}};
+    if (s.few_warps) return backward_teams<T, V, 4, EDGE, GATES, kFewWarps>(a, p, s.team);
     if (s.team_items == 2) return backward_teams<T, V, 2, EDGE, GATES>(a, p, s.team);
     if (s.team_items == 4) return backward_teams<T, V, 4, EDGE, GATES>(a, p, s.team);
     if constexpr (V == 4) return backward_teams<T, V, 8, EDGE, GATES>(a, p, s.team);

@@ -309,6 +309,22 @@ def test_backward(P, ctx, dtype, rows, hidden, post, gate):
         assert v is None or torch.equal(v, again[k])
 
 
+@pytest.mark.parametrize("dtype,hidden", [(0, 2048), (0, 2041), (0, 4090), (1, 4096), (1, 4089), (1, 7168), (1, 8181)])
+@pytest.mark.parametrize("gate", [None, "columns", "rows"])
+def test_backward_of_many_rows(P, ctx, dtype, hidden, gate):
+    """More than 32 rows an SM, of about four, seven and eight warps of four windows each."""
+    rows = 5003
+    i = inputs(rows, hidden, dtype, gate != "rows", gate, True, seed=85)
+    dy, dtotal, total = (randn(rows, hidden, seed=s, dtype=T[dtype]) for s in (95, 96, 97))
+    o = check_backward(P, ctx, i, dy, dtotal, total, dtype, 0.9, 0.25, gate == "rows")
+    again = run_backward(P, ctx, i, dy, dtotal, total, dtype, 0.9, 0.25, gate == "rows")
+    for k, v in o.items():
+        assert v is None or torch.equal(v, again[k])
+    if gate == "columns":
+        i = inputs(rows, hidden, dtype, True, "rows", True, 86, 1, 1)    # rows out of step
+        check_backward(P, ctx, i, dy, None, total, dtype, 1.0, 0.5, True)
+
+
 @pytest.mark.parametrize("dtype", [0, 1], ids=["f32", "bf16"])
 @pytest.mark.parametrize("gate", [None, "columns", "rows"])
 def test_backward_of_total_alone(P, ctx, dtype, gate):
