@@ -187,10 +187,11 @@ purlin_status purlin_dispatch_rows(purlin_ctx *ctx, const void *x, size_t ldx,
     if (st != PURLIN_OK) return st;
     ldx = ldx ? ldx : cols;
     ldo = ldo ? ldo : cols;
-    if (bad_ld(ldx, cols) || bad_ld(ldo, cols) || (scales != nullptr) != (out_scales != nullptr))
-        return PURLIN_ERR_INVALID_ARG;
+    if (bad_ld(ldx, cols) || bad_ld(ldo, cols)) return PURLIN_ERR_INVALID_ARG;
     if (tokens == 0 || cols == 0) return ctx ? PURLIN_OK : PURLIN_ERR_INVALID_ARG;
-    if (x == nullptr || place == nullptr || (out == nullptr && out_rows > 0))
+    // (arrays of no rows may be missing)
+    if (x == nullptr || place == nullptr || (scales == nullptr && out_scales != nullptr) ||
+        (out_rows > 0 && (out == nullptr || (scales != nullptr) != (out_scales != nullptr))))
         return PURLIN_ERR_INVALID_ARG;
     const size_t es = (size_t)size_of(dtype), slots = tokens * (size_t)top_k;
     if (misaligned(x, es) || misaligned(out, es) || misaligned(place, 4) ||

@@ -14,6 +14,11 @@
 // the chosen, the last of them and what is left, the last group kept and the rest) are
 // no further apart than that, and not of the same logit and bias, what is near the
 // border is computed again in binary64 and ranked by that: about one row in a thousand.
+//
+// Bound by the issue of instructions, about a thousand a token of 256 experts in eight
+// groups (16384 tokens, sigmoid, bias, four groups, top 8: 25 us, 72 % of the issue
+// slots; the logits' bytes are 2.6).  Fewer lanes a token, 8 or 16, leave more experts to
+// a lane and the work of its second best among the chosen: 32 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -327,6 +327,22 @@ def test_nothing_to_do(P, ctx):
     assert not bool(dw.any())
 
 
+def test_scales_of_no_rows(P, ctx):
+    """An empty tensor has no address: no tokens, or no rows for them, is not a
+    scale that was left out."""
+    from collective_datapath_atom_gb300 import torch_api
+
+    def place(*shape):
+        return torch.full(shape, -1, device="cuda", dtype=torch.int32)
+
+    x, s = torch.ones(3, 16, device="cuda"), torch.ones(3, device="cuda")
+    out, scales = torch_api.dispatch_rows(x[:0], place(0, 2), ctx, out_rows=4, scales=s[:0])
+    assert out.shape == (4, 16) and not bool(out.any()) and not bool(scales.any())
+    out, scales = torch_api.dispatch_rows(x, place(3, 2), ctx, out_rows=0, scales=s)
+    assert out.shape == (0, 16) and scales.shape == (0,)
+    P.purlin_check(ctx)
+
+
 def test_offsets_past_32_bits(P, ctx):
     """Rows behind 2^31 elements (2^32 bytes) of a buffer."""
     rows, cols = 140_000, 16_384
