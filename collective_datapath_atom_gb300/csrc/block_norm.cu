@@ -303,8 +303,8 @@ cudaError_t try_teams(const BlockNormArgs &a, const BlockParams &b, bool *done) 
     const bool factors = a.post_weight || (a.gate && !GATES);
     const auto shape = [&](int items) {
         const TeamShape s =
-            team_shape<V>(a.rows, a.hidden, EDGE, arrays, a.y != nullptr, factors, items, false, kForwardWarps,
-                          sizeof(O) == 1 ? kForwardWarps : sizeof(T) == 2 ? 12 : 8, a.sms);
+            team_shape<V>(a.rows, a.hidden, EDGE, arrays, a.y != nullptr, factors, items, false, false,
+                          kForwardWarps, sizeof(O) == 1 ? kForwardWarps : sizeof(T) == 2 ? 12 : 8, a.sms);
         *done = s.plan.warps != 0;
         return s;
     };

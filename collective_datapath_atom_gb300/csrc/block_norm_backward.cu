@@ -10,9 +10,8 @@
 // Bound by bytes where rows are many (32768 x 4096 bf16 with dtotal 265 us, 6.1 TB/s), by
 // the two chains of sums of a row where they are few (1000 x 4099 f32 with a gate a row 48
 // us: six or seven rows a block one after another, and loads off their boundaries; 4096
-// columns 33).  Of rows above 8192 bf16 or 4096 f32 columns an SM has one at a time, and
-// the columns' sums take most of its registers (4000 x 8200 bf16 191 us, 2.1 TB/s; 8192 x
-// 5120 f32 171, 5.9 TB/s).
+// columns 33).  Of rows above 8192 bf16 columns an SM has one at a time, and the columns'
+// sums take most of its registers (4000 x 16384 bf16 317 us, 2.5 TB/s; 8200 columns 152).
 #include "block_rows.cuh"
 
 namespace purlin {
@@ -275,7 +274,11 @@ block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
 // A thread holds ITEMS windows of its row, and the sums over rows of its columns.  HOLD:
 // all of the operands' windows, so that the stage is free behind the first sums'
 // barrier; else (wide rows, more windows a thread) they are read from the stage again,
-// and x's and h's alone are held behind the second one.
+// and x's and h's alone are held behind the second one.  AGAIN: not those either, the
+// widest rows' sums leave no registers for them; dt is made again for dx, from the stage
+// and from vectors in shared memory, and with them there a second stage is not worth its
+// room (4000 x 10000 bf16 188 us; held, and spilled, 198; that and two stages, the vectors
+// in global memory, 236; 4000 x 8200 152 and 192).
 // The rows are normed (dy, total and the weight are there).  Arrays of a stage: x, dy,
 // total, the gates where there are any, and dtotal.
 struct TeamParams : BlockBackwardParams {
@@ -283,7 +286,7 @@ struct TeamParams : BlockBackwardParams {
     size_t ld[5];
 };
 
-template <typename T, int V, int ITEMS, bool EDGE, bool GATES, bool HOLD, int WARPS>
+template <typename T, int V, int ITEMS, bool EDGE, bool GATES, bool HOLD, bool AGAIN, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS)
 block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __grid_constant__ TeamPlan plan) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
@@ -313,13 +316,13 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
     int turn = 0;
     for (size_t row = row0; row < p.rows; row += step, turn ^= 1) {
         ring.wait();
-        constexpr int kHeld = HOLD ? ITEMS : 1;
-        Window<T, V> xs[ITEMS], gk[kHeld], tk[kHeld], dk[kHeld], kk[kHeld];
+        constexpr int kHeld = HOLD ? ITEMS : 1, kKept = AGAIN ? 1 : ITEMS;
+        Window<T, V> xs[kKept], gk[kHeld], tk[kHeld], dk[kHeld], kk[kHeld];
         F2 xx = 0, tt = 0, nt = 0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int h = HOLD ? i : 0;
-            xs[i] = ring.window(0, i);
+            const int h = HOLD ? i : 0, x = AGAIN ? 0 : i;
+            xs[x] = ring.window(0, i);
             gk[h] = ring.window(1, i);
             tk[h] = ring.window(2, i);
             if constexpr (HOLD) {
@@ -330,7 +333,7 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
                 const F2 u = pair_of(tk[h], j);
-                xx = fma2(pair_of(xs[i], j), pair_of(xs[i], j), xx);
+                xx = fma2(pair_of(xs[x], j), pair_of(xs[x], j), xx);
                 tt = fma2(u, u, tt);
                 nt = fma2(mul2(pair_of(gk[h], j), pair_of(wk, j)), u, nt);
             }
@@ -346,10 +349,10 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         const float q = p.post ? rsqrtf(sx * inv_hidden + p.eps) : 1.f;
         const float r = rsqrtf(st * inv_hidden + p.eps);
         const float c = r * r * r * (sn * inv_hidden);
-        F2 h[ITEMS][V / 2], hx = 0;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int n = HOLD ? i : 0, e = vectors.column(i);
+        F2 h[kKept][V / 2], hx = 0;
+        // dt of a window, r dy weight - c t + dtotal; and dy t r for dweight
+        auto gradient = [&](int i, F2 (&dt)[V / 2], bool sum) {
+            const int n = HOLD ? i : 0;
             if constexpr (!HOLD) {
                 gk[n] = ring.window(1, i);
                 tk[n] = ring.window(2, i);
@@ -357,17 +360,23 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
                 if (p.dtotal) dk[n] = ring.window(kDtotal, i);
             }
             const Window<T, V> wk = vectors.weights(i);
-            F2 dt[V / 2], f[V / 2];
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) {   // r dy weight - c t, and dy t r for dweight
+            for (int j = 0; j < V / 2; ++j) {
                 const F2 u = pair_of(tk[n], j), d = mul2(pair_of(gk[n], j), both(r));
-                acc_w[i][j] = fma2(d, u, acc_w[i][j]);
+                if (sum) acc_w[i][j] = fma2(d, u, acc_w[i][j]);
                 dt[j] = fma2(d, pair_of(wk, j), mul2(u, both(-c)));
             }
             if (p.dtotal) {
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) dt[j] = add2(dt[j], pair_of(dk[n], j));
             }
+        };
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int n = HOLD ? i : 0, x = AGAIN ? 0 : i, e = vectors.column(i);
+            F2 dt[V / 2], f[V / 2];
+            gradient(i, dt, true);
+            if constexpr (AGAIN) xs[x] = ring.window(0, i);
             if (p.dresidual) {
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) f[j] = mul2(dt[j], both(p.residual_scale));
@@ -377,34 +386,50 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
             if constexpr (GATES) {
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) {
-                    h[i][j] = mul2(dt[j], mul2(f[j], mul2(pair_of(xs[i], j), both(q))));
+                    h[x][j] = mul2(dt[j], mul2(f[j], mul2(pair_of(xs[x], j), both(q))));
                     dt[j] = mul2(dt[j], pair_of(kk[n], j));
                 }
-                write_pairs<T, V, EDGE>(static_cast<T *>(p.dgate) + row * p.lddg, e, hidden, h[i]);
+                write_pairs<T, V, EDGE>(static_cast<T *>(p.dgate) + row * p.lddg, e, hidden, h[x]);
             }
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-                const F2 u = pair_of(xs[i], j);
+                const F2 u = pair_of(xs[x], j);
                 acc_s[i][j] = fma2(dt[j], mul2(u, both(q)), acc_s[i][j]);
-                h[i][j] = mul2(dt[j], f[j]);
-                hx = fma2(h[i][j], u, hx);
+                h[x][j] = mul2(dt[j], f[j]);
+                hx = fma2(h[x][j], u, hx);
             }
         }
         float k = 0.f;
         if (p.post)
             k = q * q * (team.template total<Sum>(low(hx) + high(hx), last[turn][slot]) * inv_hidden);
-        else if constexpr (!HOLD)
+        else if constexpr (!HOLD && !AGAIN)
             team.sync();
-        if constexpr (!HOLD) refill();
+        if constexpr (!HOLD && !AGAIN) refill();
         T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
+            const int x = AGAIN ? 0 : i;
+            if constexpr (AGAIN) {
+                F2 dt[V / 2], f[V / 2];
+                gradient(i, dt, false);
+                xs[x] = ring.window(0, i);
+                vectors.factor(i, f);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    if constexpr (GATES) dt[j] = mul2(dt[j], pair_of(kk[0], j));
+                    h[x][j] = mul2(dt[j], f[j]);
+                }
+            }
             if (p.post) {
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j)
-                    h[i][j] = mul2(fma2(pair_of(xs[i], j), both(-k), h[i][j]), both(q));
+                    h[x][j] = mul2(fma2(pair_of(xs[x], j), both(-k), h[x][j]), both(q));
             }
-            write_pairs<T, V, EDGE>(dx, vectors.column(i), hidden, h[i]);
+            write_pairs<T, V, EDGE>(dx, vectors.column(i), hidden, h[x]);
+        }
+        if constexpr (AGAIN) {
+            team.sync();
+            refill();
         }
         if (EDGE && plan.stages == 1) {   // the next row's ends are read at once
             ring.settle();
@@ -523,15 +548,15 @@ BlockBackwardShape block_backward_shape(const BlockNormBackwardArgs &a) {
         const int warps = (int)(warps_of(windows_of<V>(a.hidden, s.edge), 4) / 32);
         s.few_warps = warps >= 4 && warps <= kFewWarps && kFewWarps % warps <= 1 && a.rows / a.sms >= 32;
         if (s.few_warps) {
-            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, 4, true, kFewWarps,
+            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, 4, true, false, kFewWarps,
                                    kFewWarps, a.sms);
             s.grid = s.team.grid;
             if (s.team.plan.warps != 0) return s;
         }
         s.few_warps = false;
         for (s.team_items = 2; s.team_items <= 32 / V; s.team_items *= 2) {
-            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, s.team_items, true, kBackwardWarps,
-                                   kBackwardWarps, a.sms);
+            s.team = team_shape<V>(a.rows, a.hidden, s.edge, arrays, true, factors, s.team_items, true,
+                                   s.team_items == 32 / V, kBackwardWarps, kBackwardWarps, a.sms);
             s.grid = s.team.grid;
             if (s.team.plan.warps != 0) return s;
         }
@@ -557,9 +582,9 @@ BlockBackwardShape block_backward_shape(const BlockNormBackwardArgs &a) {
 
 template <typename T, int V, int ITEMS, bool EDGE, bool GATES, int WARPS = kBackwardWarps>
 cudaError_t backward_teams(const BlockNormBackwardArgs &a, const TeamParams &p, const TeamShape &s) {
-    constexpr bool HOLD = ITEMS == 2 || WARPS != kBackwardWarps;
+    constexpr bool HOLD = ITEMS == 2 || WARPS != kBackwardWarps, AGAIN = !HOLD && ITEMS * V == 32;
     static SharedMemoryLimit limit;
-    const auto kernel = block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD, WARPS>;
+    const auto kernel = block_norm_backward_team_kernel<T, V, ITEMS, EDGE, GATES, HOLD, AGAIN, WARPS>;
     const cudaError_t ready = limit.raise(kernel, kTeamSmem);
     if (ready != cudaSuccess) return ready;
     kernel<<<s.grid, s.threads, s.smem, a.stream>>>(p, s.plan);

@@ -3,6 +3,8 @@
 // with rings of rows in shared memory, and the launches' shapes.  Internal to the library.
 #pragma once
 
+#include <iterator>
+
 #define PURLIN_ROWS_ONLY
 #include "rms_norm.cu"
 
@@ -411,7 +413,8 @@ struct TeamShape {
 
 // Teams with `items` windows a thread, `arrays` operands a stage, and two stages at
 // least; vectors that the rows leave no room for are read from global memory, and last a
-// ring has one stage.  Teams: `least_warps` an SM, which the arithmetic wants, and rows
+// ring has one stage.  vectors_first: that comes before, where the vectors are read again
+// and again in a row.  Teams: `least_warps` an SM, which the arithmetic wants, and rows
 // for about 100 KB on their way; reads that run further ahead of the writes slow both
 // down (forward 16384 x 4096 bf16: three teams of two stages, 98 KB, 91 us, four 104).
 // joins: the teams' sums over rows are added up in shared memory, two floats a column.
@@ -420,31 +423,35 @@ constexpr size_t kTeamFlight = 100 * 1024, kRingFlight = 128 * 1024;
 
 template <int V>
 TeamShape team_shape(size_t rows, size_t hidden, bool edge, int arrays, bool weight, bool factors, int items,
-                     bool joins, int block_warps, int least_warps, int sms) {
+                     bool joins, bool vectors_first, int block_warps, int least_warps, int sms) {
     TeamShape s;
     if (rows < (size_t)sms) return s;
     const int warps = (int)(warps_of(windows_of<V>(hidden, edge), items) / 32);
     if (warps > std::min(kTeamWarps, block_warps)) return s;
     const size_t windows = (size_t)items * warps * 32;
     const size_t stage = windows * 16 * (size_t)arrays, room = kTeamSmem;
-    for (int want = 2; want >= 1; --want)
-        for (int drop = 0; drop < 3; ++drop) {
-            if (want == 1 && drop < 2) continue;   // the vectors go first
-            const bool ws = weight && drop < 2, fs = factors && drop < 1;
-            const size_t vectors = windows * ((ws ? 16 : 0) + (fs ? 4 * V : 0));
-            const size_t some = std::max<size_t>((least_warps + warps - 1) / warps, kTeamFlight / (2 * stage));
-            for (size_t teams = std::min({some, (size_t)(block_warps / warps), (rows + sms - 1) / sms}); teams >= 1; --teams) {
-                if (vectors + teams * want * stage > room) continue;
-                if (joins && teams > 1 && vectors + teams * want * stage < 8 * hidden) continue;
-                const size_t stages = std::min({(size_t)kMaxStages, (room - vectors) / (teams * stage),
-                                                std::max<size_t>(want, kRingFlight / (teams * stage))});
-                s.plan = TeamPlan{warps, (int)stages, arrays, ws, fs};
-                s.threads = (unsigned)(teams * warps * 32);
-                s.smem = vectors + teams * stages * stage;
-                s.grid = (unsigned)std::max<size_t>((size_t)sms / V * V, V);
-                return s;
-            }
+    // stages at least, and vectors that are left in global memory
+    constexpr int kRowsFirst[][2] = {{2, 0}, {2, 1}, {2, 2}, {1, 2}};
+    constexpr int kVectorsFirst[][2] = {{2, 0}, {1, 0}, {2, 1}, {1, 1}, {1, 2}};
+    const auto *tries = vectors_first ? kVectorsFirst : kRowsFirst;
+    const int most = vectors_first ? (int)std::size(kVectorsFirst) : (int)std::size(kRowsFirst);
+    for (int n = 0; n < most; ++n) {
+        const int want = tries[n][0], drop = tries[n][1];
+        const bool ws = weight && drop < 2, fs = factors && drop < 1;
+        const size_t vectors = windows * ((ws ? 16 : 0) + (fs ? 4 * V : 0));
+        const size_t some = std::max<size_t>((least_warps + warps - 1) / warps, kTeamFlight / (2 * stage));
+        for (size_t teams = std::min({some, (size_t)(block_warps / warps), (rows + sms - 1) / sms}); teams >= 1; --teams) {
+            if (vectors + teams * want * stage > room) continue;
+            if (joins && teams > 1 && vectors + teams * want * stage < 8 * hidden) continue;
+            const size_t stages = std::min({(size_t)kMaxStages, (room - vectors) / (teams * stage),
+                                            std::max<size_t>(want, kRingFlight / (teams * stage))});
+            s.plan = TeamPlan{warps, (int)stages, arrays, ws, fs};
+            s.threads = (unsigned)(teams * warps * 32);
+            s.smem = vectors + teams * stages * stage;
+            s.grid = (unsigned)std::max<size_t>((size_t)sms / V * V, V);
+            return s;
         }
+    }
     return s;
 }
 
