@@ -458,20 +458,25 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         });
         return;
     }
-    // the teams' sums, team by team, where the vectors and rows lay
+    // the teams' sums, where the vectors and rows lay, added up in the teams' order
     float *joined = reinterpret_cast<float *>(smem());
+    __syncthreads();
     for (int g = 0; g < teams; ++g) {
-        __syncthreads();
         if (team.index == g)
             each([&](int e, float w, float s) {
-                joined[e] = g == 0 ? w : joined[e] + w;
-                joined[hidden + e] = g == 0 ? s : joined[hidden + e] + s;
+                joined[2 * g * hidden + e] = w;
+                joined[(2 * g + 1) * hidden + e] = s;
             });
     }
     __syncthreads();
     for (int e = (int)threadIdx.x; e < hidden; e += (int)blockDim.x) {
-        pw[e] = joined[e];
-        if (p.sums) ps[e] = joined[hidden + e];
+        for (int n = 0; n < (p.sums ? 2 : 1); ++n) {
+            const float *from = joined + n * hidden + e;
+            float v = 0.f;
+#pragma unroll 1
+            for (int g = 0; g < teams; ++g, from += 2 * hidden) v += *from;
+            (n == 0 ? pw : ps)[e] = v;
+        }
     }
 }
 

@@ -417,7 +417,8 @@ struct TeamShape {
 // and again in a row.  Teams: `least_warps` an SM, which the arithmetic wants, and rows
 // for about 100 KB on their way; reads that run further ahead of the writes slow both
 // down (forward 16384 x 4096 bf16: three teams of two stages, 98 KB, 91 us, four 104).
-// joins: the teams' sums over rows are added up in shared memory, two floats a column.
+// joins: the teams' sums over rows are added up in shared memory, two floats a column
+// and team.
 // block_warps: of a block at most, 32 at most.
 constexpr size_t kTeamFlight = 100 * 1024, kRingFlight = 128 * 1024;
 
@@ -442,7 +443,7 @@ TeamShape team_shape(size_t rows, size_t hidden, bool edge, int arrays, bool wei
         const size_t some = std::max<size_t>((least_warps + warps - 1) / warps, kTeamFlight / (2 * stage));
         for (size_t teams = std::min({some, (size_t)(block_warps / warps), (rows + sms - 1) / sms}); teams >= 1; --teams) {
             if (vectors + teams * want * stage > room) continue;
-            if (joins && teams > 1 && vectors + teams * want * stage < 8 * hidden) continue;
+            if (joins && teams > 1 && vectors + teams * want * stage < 8 * hidden * teams) continue;
             const size_t stages = std::min({(size_t)kMaxStages, (room - vectors) / (teams * stage),
                                             std::max<size_t>(want, kRingFlight / (teams * stage))});
             s.plan = TeamPlan{warps, (int)stages, arrays, ws, fs};
