@@ -30,6 +30,7 @@ struct BlockBackwardParams {
     const void *dy, *dtotal, *x, *total, *post, *gate, *weight;
     void *dx, *dresidual, *dgate;   // dgate: rows, or null
     float *partial;                 // gridDim.x rows for dweight, then as many for S
+    uint32_t pitch;                 // of those rows, which start a block's phase early
     size_t lddy, lddt, ldx, ldt, ldg, lddx, lddr, lddg, rows;
     uint32_t hidden, phase;
     float block_scale, residual_scale, eps;
@@ -37,13 +38,25 @@ struct BlockBackwardParams {
     unsigned long long *err;
 };
 
+// A window's sums over rows to their place, on 16-byte boundaries where V is above 1.
+template <int V>
+__device__ __forceinline__ void write_sums(float *to, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *to = v[0];
+    } else {
+#pragma unroll
+        for (int n = 0; n < V / 4; ++n)
+            reinterpret_cast<float4 *>(to)[n] = make_float4(v[4 * n], v[4 * n + 1], v[4 * n + 2], v[4 * n + 3]);
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(1024)
 block_norm_backward_long_kernel(const __grid_constant__ BlockBackwardParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched
     __shared__ float sums[4][32];
-    float *pw = p.partial + (size_t)blockIdx.x * p.hidden;
-    float *ps = p.partial + ((size_t)gridDim.x + blockIdx.x) * p.hidden;
+    float *pw = p.partial + (size_t)blockIdx.x * p.pitch;
+    float *ps = pw + (size_t)gridDim.x * p.pitch;
     for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
         if (p.weight) pw[e] = 0.f;
         if (p.sums) ps[e] = 0.f;
@@ -236,8 +249,8 @@ block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
             write_window<T, V, EDGE>(dx, e0 + i * estep, hidden, h[i]);
         }
     }
-    float *pw = p.partial + (size_t)blockIdx.x * hidden;
-    float *ps = p.partial + ((size_t)gridDim.x + blockIdx.x) * hidden;
+    float *pw = p.partial + (size_t)blockIdx.x * p.pitch;
+    float *ps = pw + (size_t)gridDim.x * p.pitch;
     if (blockDim.y > 1) {   // the warps' sums, warp by warp
         for (unsigned y = 0; y < blockDim.y; ++y) {
             if (threadIdx.y == y) {
@@ -261,14 +274,12 @@ block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
         return;
     }
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int e = e0 + i * estep + j;
-            if (e < 0 || e >= hidden) continue;
-            if (normed) pw[e] = acc_w[i][j];
-            if (p.sums) ps[e] = acc_s[i][j];
-        }
+    for (int i = 0; i < ITEMS; ++i) {
+        if (e0 + i * estep >= hidden) continue;
+        const int at = (int)threadIdx.x * V + i * estep;
+        if (normed) write_sums(pw + at, acc_w[i]);
+        if (p.sums) write_sums(ps + at, acc_s[i]);
+    }
 }
 
 // A thread holds ITEMS windows of its row, and the sums over rows of its columns.  HOLD:
@@ -438,73 +449,74 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         ring.next();
     }
     if (team.thread == 0) ring.drain();
-    float *pw = p.partial + (size_t)blockIdx.x * hidden;
-    float *ps = p.partial + ((size_t)gridDim.x + blockIdx.x) * hidden;
-    auto each = [&](auto to) {   // the thread's columns and their sums
+    float *pw = p.partial + (size_t)blockIdx.x * p.pitch;
+    float *ps = pw + (size_t)gridDim.x * p.pitch;
+    auto put = [&](float *w, float *s) {   // the thread's sums, from its columns' phase on
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
+        for (int i = 0; i < ITEMS; ++i) {
+            if (vectors.column(i) >= hidden) continue;
+            const int at = vectors.column(i) + phase;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int e = vectors.column(i) + j;
-                if (e >= 0 && e < hidden)
-                    to(e, j % 2 ? high(acc_w[i][j / 2]) : low(acc_w[i][j / 2]),
-                       j % 2 ? high(acc_s[i][j / 2]) : low(acc_s[i][j / 2]));
+            for (int n = 0; n < V / 4; ++n) {
+                const F2 *a = &acc_w[i][2 * n], *b = &acc_s[i][2 * n];
+                reinterpret_cast<float4 *>(w + at)[n] = make_float4(low(a[0]), high(a[0]), low(a[1]), high(a[1]));
+                if (p.sums)
+                    reinterpret_cast<float4 *>(s + at)[n] = make_float4(low(b[0]), high(b[0]), low(b[1]), high(b[1]));
             }
+        }
     };
     if (teams == 1) {
-        each([&](int e, float w, float s) {
-            pw[e] = w;
-            if (p.sums) ps[e] = s;
-        });
+        put(pw, ps);
         return;
     }
     // the teams' sums, where the vectors and rows lay, added up in the teams' order
     float *joined = reinterpret_cast<float *>(smem());
+    const int pitch = (int)p.pitch;
     __syncthreads();
-    for (int g = 0; g < teams; ++g) {
-        if (team.index == g)
-            each([&](int e, float w, float s) {
-                joined[2 * g * hidden + e] = w;
-                joined[(2 * g + 1) * hidden + e] = s;
-            });
-    }
+    for (int g = 0; g < teams; ++g)
+        if (team.index == g) put(joined + 2 * g * pitch, joined + (2 * g + 1) * pitch);
     __syncthreads();
-    for (int e = (int)threadIdx.x; e < hidden; e += (int)blockDim.x) {
+    for (int at = 4 * (int)threadIdx.x; at < pitch; at += 4 * (int)blockDim.x) {
         for (int n = 0; n < (p.sums ? 2 : 1); ++n) {
-            const float *from = joined + n * hidden + e;
-            float v = 0.f;
+            const float *from = joined + n * pitch + at;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int g = 0; g < teams; ++g, from += 2 * hidden) v += *from;
-            (n == 0 ? pw : ps)[e] = v;
+            for (int g = 0; g < teams; ++g, from += 2 * pitch) {
+                const float4 u = *reinterpret_cast<const float4 *>(from);
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            *reinterpret_cast<float4 *>((n == 0 ? pw : ps) + at) = v;
         }
     }
 }
 
+// The blocks' sums, added up in a fixed order: dweight, and from S the gradients of
+// the weight after the block and of a column gate.  A block's sums start its rows' phase
+// into its row of them, where `phases` (V - 1, or 0) says so.
 constexpr int kJoinRows = 32;
 
-// The blocks' sums, added up in a fixed order: dweight, and from S the gradients of
-// the weight after the block and of a column gate.
 template <typename T>
 __global__ void __launch_bounds__(32 * kJoinRows)
 block_join_kernel(const float *partial, const T *post, const T *gate, float block_scale,
-                  float *dweight, float *dpost, float *dgate, uint32_t hidden, int parts) {
+                  float *dweight, float *dpost, float *dgate, uint32_t hidden, uint32_t pitch,
+                  uint32_t phase, uint32_t ld, uint32_t phases, int parts) {
     __shared__ float sums[kJoinRows][33];
     const uint32_t e = blockIdx.x * 32 + threadIdx.x;
     const bool second = blockIdx.y == (dweight ? 1 : 0);
-    if (second) partial += (size_t)parts * hidden;
+    if (second) partial += (size_t)parts * pitch;
     // launched while the rows are still being worked on: wait for all of them
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float v = 0.f;
     if (e < hidden) {
 #pragma unroll 8
-        for (int b = threadIdx.y; b < parts; b += kJoinRows) v += partial[(size_t)b * hidden + e];
+        for (uint32_t b = threadIdx.y; b < (uint32_t)parts; b += blockDim.y)
+            v += partial[(size_t)b * pitch + ((phase + ld * b) & phases) + e];
     }
     sums[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y != 0 || e >= hidden) return;
     v = sums[0][threadIdx.x];
-#pragma unroll
-    for (int k = 1; k < kJoinRows; ++k) v += sums[k][threadIdx.x];
+    for (unsigned k = 1; k < blockDim.y; ++k) v += sums[k][threadIdx.x];
     if (!second) {
         dweight[e] = v;
         return;
@@ -517,6 +529,12 @@ block_join_kernel(const float *partial, const T *post, const T *gate, float bloc
 // Whether the sum S over rows is wanted.
 bool wants_sums(const BlockNormBackwardArgs &a) {
     return a.post_weight != nullptr || (a.gate != nullptr && !a.gate_rows);
+}
+
+// A block's row of sums over rows: whole windows, whatever the phase.
+uint32_t sums_pitch(const BlockNormBackwardArgs &a) {
+    const size_t V = a.dtype == PURLIN_F32 ? 4 : 8;
+    return (uint32_t)((a.hidden + 2 * V - 2) / V * V);
 }
 
 // A backward launch: its shape, and whether it takes windows and meets edges.
@@ -629,7 +647,7 @@ cudaError_t block_norm_backward_any(const BlockNormBackwardArgs &a) {
     const bool sums = wants_sums(a);
     const BlockBackwardShape s = block_backward_shape<T>(a);
     const BlockBackwardParams p{a.dy, a.dtotal, a.x, a.total, a.post_weight, a.gate, a.weight,
-                                a.dx, a.dresidual, a.gate_rows ? a.dgate : nullptr, a.partial,
+                                a.dx, a.dresidual, a.gate_rows ? a.dgate : nullptr, a.partial, sums_pitch(a),
                                 a.lddy, a.lddt, a.ldx, a.ldt, a.ldg, a.lddx, a.lddr, a.lddg, a.rows,
                                 (uint32_t)a.hidden,
                                 (uint32_t)(reinterpret_cast<uintptr_t>(a.x) / sizeof(T) % V),
@@ -642,10 +660,15 @@ cudaError_t block_norm_backward_any(const BlockNormBackwardArgs &a) {
                           : s.windows ? backward_direct<T, V>(a, p, s)
                                       : backward_direct<T, 1>(a, p, s);
     const unsigned vectors = (a.weight ? 1 : 0) + (sums ? 1 : 0);
+    // the sums of rows in windows, unless a block adds up those of several phases itself
+    const bool phased = s.team.plan.warps != 0 || (s.windows && s.items != 0 && s.ty == 1);
     if (e != cudaSuccess || vectors == 0) return e;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)((a.hidden + 31) / 32), vectors);
-    c.blockDim = dim3(32, kJoinRows);
+    // more blocks than fit at once, or few sums to add: smaller ones (400 x 12288 bf16 51
+    // us, else 56; 2000 x 1024 18 and 17)
+    const bool small = (size_t)c.gridDim.x * vectors > 2 * (size_t)a.sms || s.grid <= kJoinRows / 4;
+    c.blockDim = dim3(32, small ? kJoinRows / 4 : kJoinRows);
     c.stream = a.stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -657,7 +680,8 @@ cudaError_t block_norm_backward_any(const BlockNormBackwardArgs &a) {
                               a.gate_rows ? (const T *)nullptr : static_cast<const T *>(a.gate),
                               a.block_scale, a.dweight, a.dpost_weight,
                               a.gate_rows ? (float *)nullptr : static_cast<float *>(a.dgate),
-                              (uint32_t)a.hidden, (int)s.grid);
+                              (uint32_t)a.hidden, p.pitch, p.phase, (uint32_t)(a.ldx % V),
+                              phased ? (uint32_t)(V - 1) : 0u, (int)s.grid);
 }
 
 }  // namespace
@@ -666,7 +690,7 @@ size_t block_norm_backward_workspace(const BlockNormBackwardArgs &a) {
     if (a.weight == nullptr && !wants_sums(a)) return 0;
     const unsigned grid = a.dtype == PURLIN_F32 ? block_backward_shape<float>(a).grid
                                                 : block_backward_shape<__nv_bfloat16>(a).grid;
-    return 2 * (size_t)grid * a.hidden * sizeof(float);
+    return 2 * (size_t)grid * sums_pitch(a) * sizeof(float);
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormBackwardArgs &a) {

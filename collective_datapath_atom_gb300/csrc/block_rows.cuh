@@ -443,7 +443,7 @@ TeamShape team_shape(size_t rows, size_t hidden, bool edge, int arrays, bool wei
         const size_t some = std::max<size_t>((least_warps + warps - 1) / warps, kTeamFlight / (2 * stage));
         for (size_t teams = std::min({some, (size_t)(block_warps / warps), (rows + sms - 1) / sms}); teams >= 1; --teams) {
             if (vectors + teams * want * stage > room) continue;
-            if (joins && teams > 1 && vectors + teams * want * stage < 8 * hidden * teams) continue;
+            if (joins && teams > 1 && vectors + teams * want * stage < 8 * (hidden + 2 * V) * teams) continue;
             const size_t stages = std::min({(size_t)kMaxStages, (room - vectors) / (teams * stage),
                                             std::max<size_t>(want, kRingFlight / (teams * stage))});
             s.plan = TeamPlan{warps, (int)stages, arrays, ws, fs};
