@@ -4,22 +4,23 @@
 // and the sums over rows  dweight = sum dy t r,  S = sum dt x q (gate):  of a column
 // gate and the weight after the block, dgate = block_scale post_weight S and
 // dpost_weight = block_scale gate S.  A thread owns the same columns in every row, so its
-// shares of the two sums stay in registers, are written once a block and added up over
+// shares of the two sums stay in registers, are written once a block, 16 bytes at a time
+// (1 x 16384 bf16 21 us; element by element, eight apart in a warp, 35), and added up over
 // the blocks in a fixed order by a second kernel: no atomics, the same bits every time.
 //
-// Bound by bytes where rows are many (32768 x 4096 bf16 with dtotal 265 us, 6.1 TB/s), by
-// the two chains of sums of a row where they are few (1000 x 4099 f32 with a gate a row 48
+// Bound by bytes where rows are many (32768 x 4096 bf16 with dtotal 263 us, 6.1 TB/s), by
+// the two chains of sums of a row where they are few (1000 x 4099 f32 with a gate a row 50
 // us: six or seven rows a block one after another, and loads off their boundaries; 4096
 // columns 33).  Of rows above 8192 bf16 columns an SM has one at a time, and the columns'
-// sums take most of its registers (4000 x 16384 bf16 317 us, 2.5 TB/s; 8200 columns 152).
+// sums take most of its registers (4000 x 16384 bf16 302 us, 2.6 TB/s; 8200 columns 141).
 #include "block_rows.cuh"
 
 namespace purlin {
 namespace {
 
 // Warps of a block of teams, with two windows a thread; or fewer, with four and with all
-// the registers there are, so that what is done once a row and thread is half as much
-// (32768 x 4096 bf16 266 us, else 281; 16384 x 7168 265 and 295; 8000 x 4096 f32 132 and
+// the registers there are, so that what is done once a row and thread is half as much (as
+// compared: 32768 x 4096 bf16 266 us, else 281; 16384 x 7168 265 and 295; 8000 x 4096 f32 132 and
 // 136). That needs rows of four warps or more (20000 x 2048, two of them, 122 and 111),
 // teams that leave one warp idle at most (8000 x 2560 f32, three idle, 122 and 95) and
 // rows enough for its slower first and last ones (2000 x 4096 37 and 35, 500 rows 21 and 19).
@@ -469,7 +470,9 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         put(pw, ps);
         return;
     }
-    // the teams' sums, where the vectors and rows lay, added up in the teams' order
+    // the teams' sums, where the vectors and rows lay, added up in the teams' order (all at
+    // once: 3000 x 512 bf16 17 us, team by team 29; the loop over teams keeps the compiler
+    // from holding what follows through the rows: 20000 x 2048 with row gates 114, else 138)
     float *joined = reinterpret_cast<float *>(smem());
     const int pitch = (int)p.pitch;
     __syncthreads();
