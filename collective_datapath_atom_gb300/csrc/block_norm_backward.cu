@@ -1,7 +1,10 @@
 // block_norm_backward.cu -- gradients of the norms around a block (block_norm.cu), with
 // n = dy weight and c = block_scale * post_weight * gate:
-//   dt = r (n - t r^2 mean(n t)) + dtotal,  h = c dt,  dx = q (h - x q^2 mean(h x)),
-// and the sums over rows  dweight = sum dy t r,  S = sum dt x q (gate):  of a column
+//   dt = r (n - t r^2 mean(n t)) + dtotal,  h = c dt,  dx = q (h - x q^2 mean(h x)).
+// The powers of r are taken one at a time: t r and r mean(n t), of the sizes of 1 and of
+// n.  r^2 or r^3 by themselves leave binary32 where dt does not (r^3 for rows of 1e13 on,
+// or of 1e-13 without an eps).
+// The sums over rows are  dweight = sum dy t r,  S = sum dt x q (gate):  of a column
 // gate and the weight after the block, dgate = block_scale post_weight S and
 // dpost_weight = block_scale gate S.  A thread owns the same columns in every row, so its
 // shares of the two sums stay in registers, are written once a block, 16 bytes at a time
@@ -87,10 +90,10 @@ block_norm_backward_long_kernel(const __grid_constant__ BlockBackwardParams p) {
         nt = reduce_row<Sum>(nt, false, sums[2]);
         const float q = post ? rsqrtf(xx / (float)p.hidden + p.eps) : 1.f;
         const float r = w ? rsqrtf(tt / (float)p.hidden + p.eps) : 0.f;
-        const float c = r * r * (nt / (float)p.hidden);
+        const float m = r * (nt / (float)p.hidden);
         auto dt_at = [&](uint32_t e) {
             float d = dtotal ? to_f32<T>(dtotal[e]) : 0.f;
-            if (w) d += r * fmaf(to_f32<T>(dy[e]), to_f32<T>(w[e]), -(to_f32<T>(total[e]) * c));
+            if (w) d = fmaf(r, fmaf(-(to_f32<T>(total[e]) * r), m, to_f32<T>(dy[e]) * to_f32<T>(w[e])), d);
             return d;
         };
         auto factor = [&](uint32_t e) {   // of dt in h
@@ -104,7 +107,7 @@ block_norm_backward_long_kernel(const __grid_constant__ BlockBackwardParams p) {
             float hx = 0.f;
             for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x)
                 hx = fmaf(dt_at(e) * factor(e), to_f32<T>(x[e]), hx);
-            k = q * q * (reduce_row<Sum>(hx, false, sums[3]) / (float)p.hidden);
+            k = q * (q * (reduce_row<Sum>(hx, false, sums[3]) / (float)p.hidden));
         }
         for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
             // every input of an element is read before an output, which may be one, is written
@@ -190,7 +193,7 @@ block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
         }
         const float q = p.post ? rsqrtf(mean_of(xx, (float)hidden, inv_hidden) + p.eps) : 1.f;
         const float r = normed ? rsqrtf(mean_of(tt, (float)hidden, inv_hidden) + p.eps) : 0.f;
-        const float c = r * r * mean_of(nt, (float)hidden, inv_hidden);
+        const float m = r * mean_of(nt, (float)hidden, inv_hidden);
         float h[ITEMS][V], hx = 0.f;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -209,9 +212,9 @@ block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
                 const Window<T, V> tk = read(p.total, p.ldt, i), gk = read(p.dy, p.lddy, i), wk = weight(i);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float u = tk.at(j), d = gk.at(j);
-                    acc_w[i][j] = fmaf(d, u * r, acc_w[i][j]);
-                    dt[j] = fmaf(r, fmaf(d, wk.at(j), -(u * c)), dt[j]);
+                    const float v = tk.at(j) * r, d = gk.at(j);
+                    acc_w[i][j] = fmaf(d, v, acc_w[i][j]);
+                    dt[j] = fmaf(r, fmaf(-v, m, d * wk.at(j)), dt[j]);
                 }
             }
             // outputs may be inputs: an element's were all read above
@@ -239,7 +242,7 @@ block_norm_backward_kernel(const __grid_constant__ BlockBackwardParams p) {
         }
         float k = 0.f;
         if (p.post)
-            k = q * q * mean_of(reduce_row<Sum>(hx, warp_only, sums[3][turn]), (float)hidden, inv_hidden);
+            k = q * (q * mean_of(reduce_row<Sum>(hx, warp_only, sums[3][turn]), (float)hidden, inv_hidden));
         T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -360,9 +363,9 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         if constexpr (HOLD) refill();
         const float q = p.post ? rsqrtf(sx * inv_hidden + p.eps) : 1.f;
         const float r = rsqrtf(st * inv_hidden + p.eps);
-        const float c = r * r * r * (sn * inv_hidden);
+        const float m = r * (sn * inv_hidden);
         F2 h[kKept][V / 2], hx = 0;
-        // dt of a window, r dy weight - c t + dtotal; and dy t r for dweight
+        // dt of a window, r (dy weight - t r m) + dtotal; and dy t r for dweight
         auto gradient = [&](int i, F2 (&dt)[V / 2], bool sum) {
             const int n = HOLD ? i : 0;
             if constexpr (!HOLD) {
@@ -374,14 +377,12 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
             const Window<T, V> wk = vectors.weights(i);
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-                const F2 u = pair_of(tk[n], j), d = mul2(pair_of(gk[n], j), both(r));
-                if (sum) acc_w[i][j] = fma2(d, u, acc_w[i][j]);
-                dt[j] = fma2(d, pair_of(wk, j), mul2(u, both(-c)));
+                const F2 v = mul2(pair_of(tk[n], j), both(r)), d = pair_of(gk[n], j);
+                if (sum) acc_w[i][j] = fma2(d, v, acc_w[i][j]);
+                dt[j] = fma2(v, both(-m), mul2(d, pair_of(wk, j)));
             }
-            if (p.dtotal) {
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) dt[j] = add2(dt[j], pair_of(dk[n], j));
-            }
+            for (int j = 0; j < V / 2; ++j) dt[j] = fma2(dt[j], both(r), p.dtotal ? pair_of(dk[n], j) : 0);
         };
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -413,7 +414,7 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
         }
         float k = 0.f;
         if (p.post)
-            k = q * q * (team.template total<Sum>(low(hx) + high(hx), last[turn][slot]) * inv_hidden);
+            k = q * (q * (team.template total<Sum>(low(hx) + high(hx), last[turn][slot]) * inv_hidden));
         else if constexpr (!HOLD && !AGAIN)
             team.sync();
         if constexpr (!HOLD && !AGAIN) refill();
