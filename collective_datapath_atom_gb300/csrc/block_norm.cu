@@ -3,7 +3,9 @@
 // c = block_scale * post_weight * gate:
 //   q = 1 / sqrt(mean(x^2) + eps),  t = residual_scale * residual + c x q,
 //   r = 1 / sqrt(mean(t^2) + eps),  y = t r weight.
-// t is rounded where it is stored alone; y is of the unrounded t.
+// t is rounded where it is stored alone; y is of the unrounded t.  Means are quotients
+// by the hidden size (mean_of), and the products above are taken in that order, in every
+// kernel: a row is the same among few rows and many but for the order of its sums.
 //
 // Bound by bytes: every operand is read once and every result written once.  Two sums over
 // the row stand between the loads and the last store, so rows are many at a time on an SM:
@@ -39,6 +41,7 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const __grid_cons
     const T *gate = static_cast<const T *>(p.gate);
     if (p.gate_rows) gate += row * p.ldg;
     const T *post = static_cast<const T *>(p.post), *w = static_cast<const T *>(p.weight);
+    const float n = (float)p.hidden, inv = 1.f / n;
     float q = 1.f;
     if (post) {
         float xx = 0.f;
@@ -46,12 +49,13 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const __grid_cons
             const float v = to_f32<T>(x[e]);
             xx = fmaf(v, v, xx);
         }
-        q = rsqrtf(reduce_row<Sum>(xx, false, sums[0]) / (float)p.hidden + p.eps);
+        q = rsqrtf(mean_of(reduce_row<Sum>(xx, false, sums[0]), n, inv) + p.eps);
     }
     auto at = [&](uint32_t e) {
-        float u = to_f32<T>(x[e]) * q * p.block_scale;
-        if (post) u *= to_f32<T>(post[e]);
-        if (gate) u *= to_f32<T>(gate[e]);
+        float c = p.block_scale;
+        if (post) c *= to_f32<T>(post[e]);
+        if (gate) c *= to_f32<T>(gate[e]);
+        const float u = c * (to_f32<T>(x[e]) * q);
         return res ? fmaf(p.residual_scale, to_f32<T>(res[e]), u) : u;
     };
     float r = 0.f, scale = 1.f;
@@ -61,7 +65,7 @@ __global__ void __launch_bounds__(1024) block_norm_long_kernel(const __grid_cons
             const float t = at(e);
             tt = fmaf(t, t, tt);
         }
-        r = rsqrtf(reduce_row<Sum>(tt, false, sums[1]) / (float)p.hidden + p.eps);
+        r = rsqrtf(mean_of(reduce_row<Sum>(tt, false, sums[1]), n, inv) + p.eps);
     }
     if constexpr (sizeof(O) == 1) {
         float most = 0.f;
@@ -91,6 +95,7 @@ block_norm_kernel(const __grid_constant__ BlockParams p) {
     if (row >= p.rows) return;   // whole warps; blockDim.y > 1 has no block barrier
     const int hidden = (int)p.hidden, estep = (int)blockDim.x * V;
     const int e0 = (int)threadIdx.x * V - (EDGE ? phase_of<V>(p.phase, p.ldx, row) : 0);
+    const float n = (float)hidden, inv = 1.f / n;
     Window<T, V> xk[ITEMS];
     float t[ITEMS][V];
     float xx = 0.f, tt = 0.f;
@@ -113,7 +118,7 @@ block_norm_kernel(const __grid_constant__ BlockParams p) {
         for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) xx = fmaf(xk[i].at(j), xk[i].at(j), xx);
-        q = rsqrtf(reduce_row<Sum>(xx, warp_only, sums[0]) / (float)hidden + p.eps);
+        q = rsqrtf(mean_of(reduce_row<Sum>(xx, warp_only, sums[0]), n, inv) + p.eps);
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
@@ -134,7 +139,7 @@ block_norm_kernel(const __grid_constant__ BlockParams p) {
         for (int i = 0; i < ITEMS; ++i) write_window<T, V, EDGE>(total, e0 + i * estep, hidden, t[i]);
     }
     if (!p.y) return;
-    const float r = rsqrtf(reduce_row<Sum>(tt, warp_only, sums[1]) / (float)hidden + p.eps);
+    const float r = rsqrtf(mean_of(reduce_row<Sum>(tt, warp_only, sums[1]), n, inv) + p.eps);
     O *y = static_cast<O *>(p.y) + row * p.ldy;
     float most = 0.f;
 #pragma unroll
@@ -190,7 +195,7 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
     ring.start();
     vectors.start();
     __syncthreads();
-    const float inv_hidden = 1.f / (float)hidden;
+    const float n = (float)hidden, inv_hidden = 1.f / n;
     int turn = 0;
     for (size_t row = row0; row < p.rows; row += step, turn ^= 1) {
         ring.wait();
@@ -203,21 +208,22 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) xx = fma2(pair_of(xk, j), pair_of(xk, j), xx);
             }
-            q = rsqrtf(team.template total<Sum>(low(xx) + high(xx), sums[0][turn][slot]) * inv_hidden + p.eps);
+            const float sum = team.template total<Sum>(low(xx) + high(xx), sums[0][turn][slot]);
+            q = rsqrtf(mean_of(sum, n, inv_hidden) + p.eps);
         }
         F2 t[ITEMS][V / 2];
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             F2 c[V / 2];
             vectors.factor(i, c);
-            const Window<T, V> xk = ring.window(0, i);
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) t[i][j] = mul2(mul2(pair_of(xk, j), both(q)), c[j]);
             if constexpr (GATES) {
                 const Window<T, V> gk = ring.window(1, i);
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) t[i][j] = mul2(t[i][j], pair_of(gk, j));
+                for (int j = 0; j < V / 2; ++j) c[j] = mul2(c[j], pair_of(gk, j));
             }
+            const Window<T, V> xk = ring.window(0, i);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) t[i][j] = mul2(mul2(pair_of(xk, j), both(q)), c[j]);
             if (p.residual) {
                 const Window<T, V> rk = ring.window(kResidual, i);
 #pragma unroll
@@ -237,8 +243,8 @@ block_norm_team_kernel(const __grid_constant__ TeamParams p, const __grid_consta
             team.sync();
             ring.refill();
         } else {
-            const float r =
-                rsqrtf(team.template total<Sum>(low(tt) + high(tt), sums[1][turn][slot]) * inv_hidden + p.eps);
+            const float sum = team.template total<Sum>(low(tt) + high(tt), sums[1][turn][slot]);
+            const float r = rsqrtf(mean_of(sum, n, inv_hidden) + p.eps);
             if (team.warps == 1) __syncwarp();
             ring.refill();
             O *y = static_cast<O *>(p.y) + row * p.ldy;

@@ -66,6 +66,7 @@ block_norm_backward_long_kernel(const __grid_constant__ BlockBackwardParams p) {
         if (p.sums) ps[e] = 0.f;
     }
     const T *post = static_cast<const T *>(p.post), *w = static_cast<const T *>(p.weight);
+    const float columns = (float)p.hidden, inv_hidden = 1.f / columns;
     for (size_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T *dy = static_cast<const T *>(p.dy) + row * p.lddy;
         const T *total = static_cast<const T *>(p.total) + row * p.ldt;
@@ -88,40 +89,38 @@ block_norm_backward_long_kernel(const __grid_constant__ BlockBackwardParams p) {
         xx = reduce_row<Sum>(xx, false, sums[0]);
         tt = reduce_row<Sum>(tt, false, sums[1]);
         nt = reduce_row<Sum>(nt, false, sums[2]);
-        const float q = post ? rsqrtf(xx / (float)p.hidden + p.eps) : 1.f;
-        const float r = w ? rsqrtf(tt / (float)p.hidden + p.eps) : 0.f;
-        const float m = r * (nt / (float)p.hidden);
+        const float q = post ? rsqrtf(mean_of(xx, columns, inv_hidden) + p.eps) : 1.f;
+        const float r = w ? rsqrtf(mean_of(tt, columns, inv_hidden) + p.eps) : 0.f;
+        const float m = r * mean_of(nt, columns, inv_hidden);
         auto dt_at = [&](uint32_t e) {
             float d = dtotal ? to_f32<T>(dtotal[e]) : 0.f;
             if (w) d = fmaf(r, fmaf(-(to_f32<T>(total[e]) * r), m, to_f32<T>(dy[e]) * to_f32<T>(w[e])), d);
             return d;
         };
-        auto factor = [&](uint32_t e) {   // of dt in h
+        auto gate_at = [&](uint32_t e) { return p.gate_rows ? to_f32<T>(gate[e]) : 1.f; };
+        auto factor = [&](uint32_t e) {   // of dt and a row's gate in h
             float f = p.block_scale;
             if (post) f *= to_f32<T>(post[e]);
-            if (gate) f *= to_f32<T>(gate[e]);
+            if (gate && !p.gate_rows) f *= to_f32<T>(gate[e]);
             return f;
         };
         float k = 0.f;
         if (post) {
             float hx = 0.f;
             for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x)
-                hx = fmaf(dt_at(e) * factor(e), to_f32<T>(x[e]), hx);
-            k = q * (q * (reduce_row<Sum>(hx, false, sums[3]) / (float)p.hidden));
+                hx = fmaf(dt_at(e) * gate_at(e) * factor(e), to_f32<T>(x[e]), hx);
+            k = q * (q * mean_of(reduce_row<Sum>(hx, false, sums[3]), columns, inv_hidden));
         }
         for (uint32_t e = threadIdx.x; e < p.hidden; e += blockDim.x) {
             // every input of an element is read before an output, which may be one, is written
-            const float dt = dt_at(e), f = factor(e), v = to_f32<T>(x[e]);
-            const float g = p.gate_rows ? to_f32<T>(gate[e]) : 1.f;
-            const float pe = post ? to_f32<T>(post[e]) : 1.f;
+            const float dt = dt_at(e), f = factor(e), g = gate_at(e), v = to_f32<T>(x[e]);
             if (w) pw[e] = fmaf(to_f32<T>(dy[e]), to_f32<T>(total[e]) * r, pw[e]);
             if (p.sums) ps[e] = fmaf(dt * g, v * q, ps[e]);
-            const float h = dt * f;
+            const float h = dt * g * f;
             if (p.dresidual)
                 static_cast<T *>(p.dresidual)[row * p.lddr + e] = from_f32<T>(p.residual_scale * dt);
             if (p.dgate)
-                static_cast<T *>(p.dgate)[row * p.lddg + e] =
-                    from_f32<T>(p.block_scale * dt * (v * q * pe));
+                static_cast<T *>(p.dgate)[row * p.lddg + e] = from_f32<T>(dt * (f * (v * q)));
             static_cast<T *>(p.dx)[row * p.lddx + e] = from_f32<T>(post ? q * fmaf(-v, k, h) : h);
         }
         __syncthreads();   // before the next row's sums
@@ -326,7 +325,7 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
     ring.start();
     vectors.start();
     __syncthreads();
-    const float inv_hidden = 1.f / (float)hidden;
+    const float columns = (float)hidden, inv_hidden = 1.f / columns;
     F2 acc_w[ITEMS][V / 2] = {}, acc_s[ITEMS][V / 2] = {};
     int turn = 0;
     for (size_t row = row0; row < p.rows; row += step, turn ^= 1) {
@@ -361,9 +360,9 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
             ring.refill();
         };
         if constexpr (HOLD) refill();
-        const float q = p.post ? rsqrtf(sx * inv_hidden + p.eps) : 1.f;
-        const float r = rsqrtf(st * inv_hidden + p.eps);
-        const float m = r * (sn * inv_hidden);
+        const float q = p.post ? rsqrtf(mean_of(sx, columns, inv_hidden) + p.eps) : 1.f;
+        const float r = rsqrtf(mean_of(st, columns, inv_hidden) + p.eps);
+        const float m = r * mean_of(sn, columns, inv_hidden);
         F2 h[kKept][V / 2], hx = 0;
         // dt of a window, r (dy weight - t r m) + dtotal; and dy t r for dweight
         auto gradient = [&](int i, F2 (&dt)[V / 2], bool sum) {
@@ -413,10 +412,12 @@ block_norm_backward_team_kernel(const __grid_constant__ TeamParams p, const __gr
             }
         }
         float k = 0.f;
-        if (p.post)
-            k = q * (q * (team.template total<Sum>(low(hx) + high(hx), last[turn][slot]) * inv_hidden));
-        else if constexpr (!HOLD && !AGAIN)
+        if (p.post) {
+            const float sum = team.template total<Sum>(low(hx) + high(hx), last[turn][slot]);
+            k = q * (q * mean_of(sum, columns, inv_hidden));
+        } else if constexpr (!HOLD && !AGAIN) {
             team.sync();
+        }
         if constexpr (!HOLD && !AGAIN) refill();
         T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
