@@ -320,11 +320,16 @@ route_kernel(const __grid_constant__ RouteParams p) {
             c = max(min(a, oa), max(c, oc));
             a = max(a, oa);
         }
-        float v = of_key(a);
+        float v = of_key(a), size = 0.f;   // size: of what v adds up
         const bool exactly = !p.bias && p.group_top == 1;   // logits, nothing to tell apart
         if (!exactly) {
             if (!p.bias) v = score(v);
-            if (p.group_top == 2 && c != 0) v += p.bias ? of_key(c) : score(of_key(c));
+            size = fabsf(v);
+            if (p.group_top == 2 && c != 0) {
+                const float second = p.bias ? of_key(c) : score(of_key(c));
+                v += second;
+                size += fabsf(second);
+            }
         }
         const uint32_t mine = a != 0 ? key_of(v) : 0;
         int rank = 0;
@@ -336,23 +341,24 @@ route_kernel(const __grid_constant__ RouteParams p) {
         const bool there = g < p.groups && mine != 0;
         bool keep = there && rank < p.top_groups;
         if (!exactly) {
-            // the last one kept, and whether another one near it is not its like
-            const unsigned last = __ballot_sync(kAll, there && rank == p.top_groups - 1);
-            if (last != 0) {
-                const int at = __ffs(last) - 1;
-                const float edge = __shfl_sync(kAll, v, at);
-                const bool close =
-                    there && near(fmaxf(v, edge), fminf(v, edge), 4.f * tol + fabsf(edge) * 0x1p-22f);
-                if (__any_sync(kAll, close && !keep)) {
-                    const uint32_t ea = __shfl_sync(kAll, a, at), ec = __shfl_sync(kAll, c, at);
-                    const bool alike = !p.bias && a == ea && c == ec;
-                    if (__any_sync(kAll, close && !alike && rank != p.top_groups - 1)) {
-                        const uint32_t edge_key = p.group_top == 2 && c != 0 ? c : a;
-                        const float edge_c = of_key(edge_key);
-                        const float under = edge_c - (2.f * tol + fabsf(edge_c) * 0x1p-22f);
-                        const uint32_t least = !p.bias ? edge_key : under == under ? key_of(under) : 1;
-                        keep = exact_groups(row, key, least, exact_scores(row, p.sigmoid, most), p, lane);
-                    }
+            // each value is off by its two choices' errors and the sum's, which go by the
+            // choices' sizes (with opposite signs the sum has none); where one kept may lie
+            // below one that is left, and they are not the like of the last one kept
+            const float off = fabsf(v) <= kMaxFinite ? 2.f * tol + size * 0x1.8p-23f : 0.f;
+            const uint32_t low = key_of(v - off), high = key_of(v + off);
+            const uint32_t kept = __reduce_min_sync(kAll, keep ? low : 0xffffffffu);
+            const uint32_t left = __reduce_max_sync(kAll, there && !keep ? high : 0);
+            const bool unsure = keep ? low <= left : there && high >= kept;
+            if (__any_sync(kAll, unsure)) {
+                const int at = __ffs(__ballot_sync(kAll, there && rank == p.top_groups - 1)) - 1;
+                const uint32_t ea = __shfl_sync(kAll, a, at), ec = __shfl_sync(kAll, c, at);
+                const bool alike = !p.bias && a == ea && c == ec;
+                if (__any_sync(kAll, unsure && !alike)) {
+                    const uint32_t edge_key = p.group_top == 2 && c != 0 ? c : a;
+                    const float edge_c = of_key(edge_key);
+                    const float under = edge_c - (2.f * tol + fabsf(edge_c) * 0x1p-22f);
+                    const uint32_t least = !p.bias ? edge_key : under == under ? key_of(under) : 1;
+                    keep = exact_groups(row, key, least, exact_scores(row, p.sigmoid, most), p, lane);
                 }
             }
         }
