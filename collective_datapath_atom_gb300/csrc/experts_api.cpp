@@ -97,7 +97,6 @@ purlin_status purlin_route(purlin_ctx *ctx, const void *logits, size_t ld, const
     a.chosen = chosen;
     a.ld = ld;
     a.tokens = tokens;
-    a.sms = ctx->sms;
     a.stream = ctx->stream;
     return done(launch_route(a));
 }
@@ -134,7 +133,6 @@ purlin_status purlin_route_backward(purlin_ctx *ctx, const float *dweights, cons
     a.ld = ld;
     a.ldd = ldd;
     a.tokens = tokens;
-    a.sms = ctx->sms;
     a.stream = ctx->stream;
     return done(launch_route_backward(a));
 }

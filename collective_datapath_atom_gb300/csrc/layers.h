@@ -143,7 +143,6 @@ struct RouteArgs {
     bool sigmoid = false, renormalise = false;
     float scale = 1;
     int dtype = 0;
-    int sms = 0;
     cudaStream_t stream = nullptr;
 };
 
