@@ -15,8 +15,6 @@ using namespace purlin::host;
 
 namespace {
 
-purlin_status done(cudaError_t e) { return e == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA; }
-
 bool bad_extents(size_t rows, size_t hidden, float eps, float block_scale, float residual_scale,
                  purlin_gate_layout layout) {
     return hidden == 0 || hidden > kMaxExtent / 2 || rows > kMaxExtent || !(eps >= 0) ||
@@ -28,12 +26,6 @@ bool bad_extents(size_t rows, size_t hidden, float eps, float block_scale, float
 bool clashes(const Matrix &out, std::initializer_list<Matrix> inputs) {
     for (const Matrix &m : inputs)
         if (overlap(out, m) && !same(out, m)) return true;
-    return false;
-}
-
-bool any_overlap(const Matrix &out, std::initializer_list<Matrix> others) {
-    for (const Matrix &m : others)
-        if (overlap(out, m)) return true;
     return false;
 }
 

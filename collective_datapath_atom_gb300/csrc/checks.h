@@ -2,8 +2,11 @@
 // (layers_api.cpp, experts_api.cpp, block_api.cpp).  Internal to the library.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/purlin.h"
 
@@ -38,6 +41,12 @@ inline bool overlap(const Matrix &a, const Matrix &b) {
     return !(d >= a.width && d + b.width <= a.pitch);
 }
 
+inline bool any_overlap(const Matrix &out, std::initializer_list<Matrix> others) {
+    for (const Matrix &m : others)
+        if (overlap(out, m)) return true;
+    return false;
+}
+
 // The same elements in the same places: allowed where a thread reads an
 // element before it writes it.
 inline bool same(const Matrix &a, const Matrix &b) {
@@ -47,6 +56,8 @@ inline bool same(const Matrix &a, const Matrix &b) {
 inline bool misaligned(const void *p, size_t to) {
     return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0;
 }
+
+inline purlin_status done(cudaError_t e) { return e == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA; }
 
 inline bool bad_ld(size_t ld, size_t cols) { return ld < cols || ld > kMaxPitch; }
 

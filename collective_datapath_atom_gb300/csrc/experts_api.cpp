@@ -4,7 +4,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <initializer_list>
 
 #include "checks.h"
 #include "host.h"
@@ -15,16 +14,8 @@ using namespace purlin::host;
 
 namespace {
 
-purlin_status done(cudaError_t e) { return e == cudaSuccess ? PURLIN_OK : PURLIN_ERR_CUDA; }
-
 // A device array of n 32-bit values.
 Matrix words(const void *p, size_t n) { return matrix(p, 1, n, n, PURLIN_F32); }
-
-bool any_overlap(const Matrix &out, std::initializer_list<Matrix> others) {
-    for (const Matrix &m : others)
-        if (overlap(out, m)) return true;
-    return false;
-}
 
 // The router's fields, checked, as launch arguments.
 purlin_status read_router(const purlin_router *r, purlin_dtype dtype, RouteArgs *a) {
