@@ -10,8 +10,8 @@
 // Bound by bytes: every operand is read once and every result written once.  Two sums over
 // the row stand between the loads and the last store, so rows are many at a time on an SM:
 // persistent blocks of teams of warps, a team a row, with rings of rows that bulk copies
-// fill (16384 x 7168 bf16 with the residual to e4m3 135 us, 6.1 TB/s; 16384 x 4096 bf16 98
-// us, 5.5 TB/s; two blocks an SM with a ring each 170).  Few rows, and rows whose operands
+// fill (16384 x 7168 bf16 with the residual to e4m3 133 us, 6.2 TB/s; 16384 x 4096 bf16 99
+// us, 5.4 TB/s; two blocks an SM with a ring each 170).  Few rows, and rows whose operands
 // are out of step, have a block each, and registers (1 x 4096: the launch); rows that fit
 // neither are read again, element by element.
 #include "block_rows.cuh"
@@ -166,6 +166,11 @@ block_norm_kernel(const __grid_constant__ BlockParams p) {
 // operands that it reads from the stage again.  Holding those, which frees the stage a
 // barrier earlier, needs 128 registers, and three teams of seven warps are worth more
 // than early loads (16384 x 7168 bf16 to e4m3 140 us, two teams that hold them 153).
+// With 16 / 21 / 24 warps of a block at most (us, 8192 rows, 16384 of 7168 columns; of 24 a
+// thread has fewer registers):
+//   bf16 to e4m3: 4096 50 / 49 / 50, 5120 58 / 58 / 62, 6144 74 / 66 / 70, 7168 138 / 133 / 139,
+//   8192 86 / 90 / 96;  bf16: 4096 54 / 53 / 52, 6144 76 / 74 / 73;  f32: 4096 89 / 100 / 89,
+//   5120 119 / 125 / 122;  f32 to e4m3: 5120 122 / 98 / 93, 6144 130 / 121 / 128.
 constexpr int kForwardWarps = 21;
 
 // Operands of the rows, in the order of their arrays in a stage: x, the gates where
@@ -307,6 +312,10 @@ cudaError_t try_teams(const BlockNormArgs &a, const BlockParams &b, bool *done) 
     TeamParams p{b, {a.x, GATES ? a.gate : a.residual, a.residual}, {a.ldx, GATES ? a.ldg : a.ldr, a.ldr}};
     const int arrays = 1 + (a.residual ? 1 : 0) + (GATES ? 1 : 0);
     const bool factors = a.post_weight || (a.gate && !GATES);
+    // Warps that the arithmetic wants: the maximum and the quotients of e4m3 all of them
+    // (8192 x 4096 bf16 to e4m3 49 us, with 12 55; 6144 66 and 78), rows of f32, of which
+    // fewer are as many bytes, the fewest (4096 100 us with 8, 12 or 21); bf16 4096 53 with 12
+    // or 8, 57 with 21, 6144 74 and 80, 8192 104, 107 with 8, 5120 68, 64 with 8.
     const auto shape = [&](int items) {
         const TeamShape s =
             team_shape<V>(a.rows, a.hidden, EDGE, arrays, a.y != nullptr, factors, items, false, false,

@@ -11,11 +11,12 @@
 // (1 x 16384 bf16 21 us; element by element, eight apart in a warp, 35), and added up over
 // the blocks in a fixed order by a second kernel: no atomics, the same bits every time.
 //
-// Bound by bytes where rows are many (32768 x 4096 bf16 with dtotal 263 us, 6.1 TB/s), by
-// the two chains of sums of a row where they are few (1000 x 4099 f32 with a gate a row 50
-// us: six or seven rows a block one after another, and loads off their boundaries; 4096
-// columns 33).  Of rows above 8192 bf16 columns an SM has one at a time, and the columns'
-// sums take most of its registers (4000 x 16384 bf16 302 us, 2.6 TB/s; 8200 columns 141).
+// Bound by bytes where rows are many (32768 x 4096 bf16 with dtotal 260 us, 6.2 TB/s), by
+// the two chains of sums of a row where they are few.  Of rows above 8192 bf16 or 4096 f32
+// columns an SM has one at a time: two windows a thread would take more than sixteen warps,
+// so nine do the row with four, which hold none of its operands (1000 x 4099 f32 with a gate
+// a row 50 us, 4096 columns, sixteen warps that hold them, 33; 4000 x 8200 bf16 142), and of
+// the widest the columns' sums take most of the registers (4000 x 16384 306, 2.6 TB/s).
 #include "block_rows.cuh"
 
 namespace purlin {
@@ -23,12 +24,16 @@ namespace {
 
 // Warps of a block of teams, with two windows a thread; or fewer, with four and with all
 // the registers there are, so that what is done once a row and thread is half as much (as
-// compared: 32768 x 4096 bf16 266 us, else 281; 16384 x 7168 265 and 295; 8000 x 4096 f32 132 and
-// 136). That needs rows of four warps or more (20000 x 2048, two of them, 122 and 111),
-// teams that leave one warp idle at most (8000 x 2560 f32, three idle, 122 and 95) and
-// rows enough for its slower first and last ones (2000 x 4096 37 and 35, 500 rows 21 and 19).
+// compared: 32768 x 4096 bf16 261 us, else 274; 16384 x 7168 257 and 295; 8000 x 4096 f32 128 and
+// 134). That needs rows of four warps or more (20000 x 2048, two of them, 114 and 109),
+// teams that leave one warp idle at most (8000 x 2560 f32, three idle, 115 and 97) and
+// rows enough for its slower first and last ones (2000 x 4096 35 and 33, 500 rows 19 and 17).
 constexpr int kBackwardWarps = 16, kFewWarps = 8;
-constexpr size_t kDirectThreadsSm = 512;   // rows on the registers: threads an SM
+// Rows on the registers, threads an SM: more of them share out what is one row after
+// another, and leave more sums to join (512, 256 and 1024: 8000 x 4096 bf16 out of step 547,
+// 965 and 559 us; without the second norm 8000 x 512 27, 31 and 35, 2000 x 2048 25, 36 and 29;
+// 2000 x 1024 out of step 37, 57 and 29).
+constexpr size_t kDirectThreadsSm = 512;
 
 struct BlockBackwardParams {
     const void *dy, *dtotal, *x, *total, *post, *gate, *weight;

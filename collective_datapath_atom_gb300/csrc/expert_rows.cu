@@ -12,8 +12,8 @@
 // row and all of the token's places: dispatch loads once and stores top_k times, combine
 // adds up the rows in their order in binary32, with many threads an SM for the loads in
 // flight.  16384 tokens of eight places: dispatch of 7168 bytes and a scale 158 us (6.7
-// TB/s) and the order 13; combine of 7168 bf16 348 us (6.1 TB/s); its backward pass of 4096
-// bf16 356 us (6.4 TB/s).
+// TB/s) and the order 8.6 on the device, 13 with its two launches; combine of 7168 bf16 348
+// us (6.1 TB/s); its backward pass of 4096 bf16 356 us (6.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +30,10 @@ constexpr unsigned kAll = 0xffffffffu;
 // ------------------------------------------------------------------- order --
 
 constexpr int kOrderThreads = 256, kOrderWarps = kOrderThreads / 32;
-constexpr int kOrderSlots = 2048;   // least slots of a block
+// Least slots of a block.  Fewer are more blocks, each of which adds up all the others'
+// counts (131072 slots of 256 experts 8.6 us on the device, with 1024 10.0, with 4096 10.6;
+// 4096 slots 6.9, 6.2 and 7.6; 2048, one launch, 4.5, 5.6 and 4.6).
+constexpr int kOrderSlots = 2048;
 
 struct OrderParams {
     const int32_t *chosen;
@@ -513,6 +516,10 @@ cudaError_t dispatch_typed(const RowsArgs &a) {
     RowsParams p;
     return by_width<ES, kLeast>(params(a, ES, kLeast, &p), [&](auto width) {
         constexpr int W = decltype(width)::value;
+        // four windows a thread where blocks are many and rows fill them: a token's places
+        // are read once for four times the bytes (16384 x 7168 e4m3 to one place each 37.6 us,
+        // a window a thread 41.1; two places 55.3 and 55.5; eight 164 and 162; 128 tokens of
+        // eight 6.2 and 4.2)
         const bool many = a.tokens * p.windows >= (size_t)a.sms * 8192 && p.windows >= 256;
         unsigned grid;
         dim3 block;

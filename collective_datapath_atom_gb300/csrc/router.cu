@@ -13,11 +13,13 @@
 // an error of at most `tol`, and where two that matter to the answer (neighbours among
 // the chosen, the last of them and what is left, the last group kept and the rest) are
 // no further apart than that, and not of the same logit and bias, what is near the
-// border is computed again in binary64 and ranked by that: about one row in a thousand.
+// border is computed again in binary64 and ranked by that: about two rows in a thousand.
+// What binary64 does not tell apart, as scores of logits above 37 with a bias, are equal
+// values.
 //
 // Bound by the issue of instructions, about a thousand a token of 256 experts in eight
 // groups (16384 tokens, sigmoid, bias, four groups, top 8: 25 us, 72 % of the issue
-// slots; the logits' bytes are 2.6).  Fewer lanes a token, 8 or 16, leave more experts to
+// slots; the logits' bytes are 2.6; bf16 the same).  Fewer lanes a token, 8 or 16, leave more experts to
 // a lane and the work of its second best among the chosen: 32 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

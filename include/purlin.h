@@ -454,9 +454,11 @@ typedef struct purlin_router {
  * largest c are chosen.  chosen[token][j] is the j-th of them (falling c) and
  *   weights[token][j] = scale * s[chosen] (/ the sum of the chosen s).
  * The bias (F32, `experts` values) evens out the load: it decides the choice
- * and is not in the weights.  The choice is that of exact values: where
- * binary32 does not tell two apart, binary64 does; equal values go to the
- * lowest index.  Renormalised weights are those of the logits, also where the
+ * and is not in the weights.  The choice is that of exact values as far as
+ * binary64: without a bias and with group_top 1 the logits are compared,
+ * else values that binary32 does not tell apart are computed in binary64, and
+ * those that are equal there go to the lowest index (with a bias, sigmoids of
+ * logits above 37 all are 1).  Renormalised weights are those of the logits, also where the
  * scores themselves would be too small for binary32.
  * Masks: an expert whose logit is -inf has score 0 and is not chosen, nor is
  * one whose bias is -inf or NaN.  Where fewer than top_k are left, the last
